@@ -59,6 +59,24 @@ class Info(ctypes.Structure):
                 ("backward_workspace_bytes", ctypes.c_size_t)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("dim", ctypes.c_int * 3), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double * 3), ("original", ctypes.c_double * 3),
+                ("slow", ctypes.c_double), ("fast", ctypes.c_double), ("amplitude", ctypes.c_double),
+                ("offset", ctypes.c_int * 3), ("pos", ctypes.c_void_p)]
+
+
+class _ScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("dist_t", ctypes.c_float), ("dist_h", ctypes.c_float),
+                ("dist_w", ctypes.c_float), ("slopes", ctypes.c_void_p), ("causal", ctypes.c_int),
+                ("prefix", ctypes.c_void_p), ("doc", ctypes.c_void_p)]
+
+
+class _ModInfo(ctypes.Structure):
+    _fields_ = [("scores_workspace_bytes", ctypes.c_size_t), ("forward_workspace_bytes", ctypes.c_size_t),
+                ("backward_workspace_bytes", ctypes.c_size_t), ("layer_workspace_bytes", ctypes.c_size_t)]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libbsattn.so not built ({path}); run "
@@ -89,6 +107,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "attn_schedule_plan": [P, I, ctypes.POINTER(P)],
         "attn_schedule_workspace_bytes": [P, ctypes.POINTER(Z)],
         "attn_schedule_layer": [P, I, P, P, P, P, P, P, P, P, Z, P],
+        "attn_rope": [P, ctypes.POINTER(_Rope), P, P, P, P, P, P, I, P],
+        "attn_mod_info": [P, ctypes.POINTER(_ModInfo)],
+        "attn_mod_scores": [P, ctypes.POINTER(_ScoreMod), P, P, P, Z, P],
+        "attn_forward_mod": [P, ctypes.POINTER(_ScoreMod), P, P, P, P, P, P, P, P, P, P, Z, P],
+        "attn_forward_natural_mod": [P, ctypes.POINTER(_ScoreMod), P, P, P, P, P, P, P, P, P, P, Z, P],
+        "attn_backward_mod": [P, ctypes.POINTER(_ScoreMod), P, P, P, P, P, P, P, P, P, P, P, P, P, Z, P],
+        "attn_layer_mod": [P, ctypes.POINTER(_Rope), ctypes.POINTER(_ScoreMod), P, P, P, P, P, P, P, P, Z, P],
         "attn_testing_force_timeout": [I],
         "attn_testing_set_error_word": [P, I],
     }
@@ -108,7 +133,8 @@ EXPORTED = ("attn_plan_create", "attn_plan_destroy", "attn_plan_info", "attn_sta
             "attn_forward", "attn_forward_natural",
             "attn_layer", "attn_check_device_status", "attn_schedule_create", "attn_schedule_destroy",
             "attn_schedule_plan", "attn_schedule_workspace_bytes", "attn_schedule_layer",
-            "attn_backward", "attn_testing_force_timeout", "attn_testing_set_error_word")
+            "attn_backward", "attn_rope", "attn_mod_info", "attn_mod_scores", "attn_forward_mod",
+            "attn_forward_natural_mod", "attn_backward_mod", "attn_layer_mod", "attn_testing_force_timeout", "attn_testing_set_error_word")
 
 
 def _check(code: int, where: str):
@@ -159,6 +185,8 @@ class Plan:
         info = Info()
         _check(_lib.attn_plan_info(h, ctypes.byref(info)), "attn_plan_info")
         self.info = info
+        self.mod_info = _ModInfo()
+        _check(_lib.attn_mod_info(h, ctypes.byref(self.mod_info)), "attn_mod_info")
         self.B, self.heads, self.D = B, heads, head_dim
         self.T, self.H, self.W = T, H, W
         self.L = T * H * W
@@ -198,8 +226,56 @@ class Plan:
         nbytes = {"select": self.info.select_workspace_bytes,
                   "forward": self.info.forward_workspace_bytes,
                   "layer": self.info.layer_workspace_bytes,
-                  "backward": self.info.backward_workspace_bytes}[which]
+                  "backward": self.info.backward_workspace_bytes,
+                  "mod_scores": self.mod_info.scores_workspace_bytes,
+                  "mod_forward": self.mod_info.forward_workspace_bytes,
+                  "mod_backward": self.mod_info.backward_workspace_bytes,
+                  "mod_layer": self.mod_info.layer_workspace_bytes}[which]
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+class Rope:
+    """Rotary positions of Q and K (bsattn_rope in include/bsattn.h): `dims`
+    features of each head turn with the token's t, h and w position. `pos`:
+    None, or int32 [B, L, 3] positions in place of the grid coordinates plus
+    `offset`."""
+
+    LAYOUTS = {"interleaved": 0, "half": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+    def __init__(self, dims, layout="interleaved", base=10000.0, scaling="none", factor=(1.0, 1.0, 1.0),
+                 original=(1.0, 1.0, 1.0), slow=1.0, fast=32.0, amplitude=1.0, offset=(0, 0, 0), pos=None):
+        self.pos = pos
+        self.raw = _Rope(self.LAYOUTS[layout] if isinstance(layout, str) else int(layout), tuple(int(d) for d in dims),
+                         self.SCALINGS[scaling] if isinstance(scaling, str) else int(scaling), float(base),
+                         tuple(float(f) for f in factor), tuple(float(x) for x in original), float(slow), float(fast),
+                         float(amplitude), tuple(int(o) for o in offset), _ptr(pos))
+
+    def _for(self, plan):
+        if self.pos is not None:
+            _want(self.pos, torch.int32, (plan.B, plan.L, 3), "pos")
+        return ctypes.byref(self.raw)
+
+
+class ScoreMod:
+    """Score rules of the attention (bsattn_score_mod in include/bsattn.h):
+    tanh cap, distance bias (`slopes` fp32 [heads], `dist` weights of the
+    distances along t, h, w), causal order of frames with a visible prefix
+    (`prefix` int32 [B]) and document ids (`doc` int32 [B, L]). Holds on to
+    its tensors."""
+
+    def __init__(self, softcap=0.0, slopes=None, dist=(1.0, 1.0, 1.0), causal=False, prefix=None, doc=None):
+        self.slopes, self.prefix, self.doc = slopes, prefix, doc
+        self.raw = _ScoreMod(float(softcap), float(dist[0]), float(dist[1]), float(dist[2]), _ptr(slopes),
+                             int(bool(causal)), _ptr(prefix), _ptr(doc))
+
+    def _for(self, plan):
+        for name, t, dtype, shape in (("slopes", self.slopes, torch.float32, (plan.heads,)),
+                                      ("prefix", self.prefix, torch.int32, (plan.B,)),
+                                      ("doc", self.doc, torch.int32, (plan.B, plan.L))):
+            if t is not None:
+                _want(t, dtype, shape, name)
+        return ctypes.byref(self.raw)
 
 
 class Schedule:
@@ -429,6 +505,103 @@ def attn_backward(plan: Plan, q_t, k_t, v_t, o_t, do_t, lse_t, idx, cnt, dq_t, d
     _check(_lib.attn_backward(plan.handle, _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(o_t), _ptr(do_t), _ptr(lse_t),
                               _ptr(idx), _ptr(cnt), _ptr(dq_t), _ptr(dk_t), _ptr(dv_t), _ptr(ws),
                               ws.numel() * ws.element_size(), _stream(stream)), "attn_backward")
+
+
+def attn_rope(plan: Plan, rope: Rope, x0, y0, x1=None, y1=None, pooled0=None, pooled1=None, transpose=False,
+              stream=None):
+    for name, t in (("x0", x0), ("y0", y0), ("x1", x1), ("y1", y1)):
+        if t is not None or name in ("x0", "y0"):
+            _want(t, torch.bfloat16, plan.natural_shape(), name)
+    for name, t in (("pooled0", pooled0), ("pooled1", pooled1)):
+        if t is not None:
+            _want(t, torch.float32, (plan.B, plan.heads, plan.N, plan.D), name)
+    _check(_lib.attn_rope(plan.handle, rope._for(plan), _ptr(x0), _ptr(y0), _ptr(x1), _ptr(y1), _ptr(pooled0),
+                          _ptr(pooled1), int(bool(transpose)), _stream(stream)), "attn_rope")
+
+
+def _ws(ws):
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def attn_mod_scores(plan: Plan, mod: ScoreMod, scores, out, ws=None, stream=None):
+    shape = (plan.B, plan.heads, plan.N, plan.N)
+    _want(scores, torch.float32, shape, "scores")
+    _want(out, torch.float32, shape, "out")
+    _check(_lib.attn_mod_scores(plan.handle, mod._for(plan), _ptr(scores), _ptr(out), *_ws(ws), _stream(stream)),
+           "attn_mod_scores")
+
+
+def _want_lists(plan, idx, cnt):
+    si, sc = plan.list_shapes()
+    _want(idx, torch.int32, si, "idx")
+    _want(cnt, torch.int32, sc, "cnt")
+
+
+def _want_scales(plan, q_scale, k_scale):
+    if plan.qk_fp8:
+        for name, t in (("q_scale", q_scale), ("k_scale", k_scale)):
+            if t is not None:
+                _want(t, torch.float32, (plan.B, plan.heads, plan.N), name)
+
+
+def attn_forward_mod(plan: Plan, mod: ScoreMod, q, k, v, idx, cnt, o_tiled, ws=None, lse=None, q_scale=None,
+                     k_scale=None, stream=None):
+    qk_dtype = torch.uint8 if plan.qk_fp8 else torch.bfloat16
+    for name, t, dtype in (("q", q, qk_dtype), ("k", k, qk_dtype), ("v", v, torch.bfloat16),
+                           ("o_tiled", o_tiled, torch.bfloat16)):
+        _want(t, dtype, plan.tiled_shape(), name)
+    _want_lists(plan, idx, cnt)
+    _want_scales(plan, q_scale, k_scale)
+    if lse is not None:
+        _want(lse, torch.float32, (plan.B, plan.heads, plan.N, plan.V), "lse")
+    _check(_lib.attn_forward_mod(plan.handle, mod._for(plan), _ptr(q), _ptr(k), _ptr(q_scale), _ptr(k_scale), _ptr(v),
+                                 _ptr(idx), _ptr(cnt), _ptr(o_tiled), _ptr(lse), *_ws(ws), _stream(stream)),
+           "attn_forward_mod")
+
+
+def attn_forward_natural_mod(plan: Plan, mod: ScoreMod, q, k, v_nat, idx, cnt, o_nat, ws=None, lse_nat=None,
+                             q_scale=None, k_scale=None, stream=None):
+    qk_dtype, qk_shape = (torch.uint8, plan.tiled_shape()) if plan.qk_fp8 else (torch.bfloat16, plan.natural_shape())
+    _want(q, qk_dtype, qk_shape, "q")
+    _want(k, qk_dtype, qk_shape, "k")
+    _want(v_nat, torch.bfloat16, plan.natural_shape(), "v_nat")
+    _want(o_nat, torch.bfloat16, plan.natural_shape(), "o_nat")
+    _want_lists(plan, idx, cnt)
+    _want_scales(plan, q_scale, k_scale)
+    if lse_nat is not None:
+        _want(lse_nat, torch.float32, (plan.B, plan.heads, plan.L), "lse_nat")
+    _check(_lib.attn_forward_natural_mod(plan.handle, mod._for(plan), _ptr(q), _ptr(k), _ptr(q_scale), _ptr(k_scale),
+                                         _ptr(v_nat), _ptr(idx), _ptr(cnt), _ptr(o_nat), _ptr(lse_nat), *_ws(ws),
+                                         _stream(stream)), "attn_forward_natural_mod")
+
+
+def attn_backward_mod(plan: Plan, mod: ScoreMod, q_t, k_t, v_t, o_t, do_t, lse_t, idx, cnt, dq_t, dk_t, dv_t, ws,
+                      d_slopes=None, stream=None):
+    for name, t in (("q", q_t), ("k", k_t), ("v", v_t), ("o", o_t), ("do", do_t), ("dq", dq_t), ("dk", dk_t),
+                    ("dv", dv_t)):
+        _want(t, torch.bfloat16, plan.tiled_shape(), name)
+    _want(lse_t, torch.float32, (plan.B, plan.heads, plan.N, plan.V), "lse")
+    _want_lists(plan, idx, cnt)
+    if d_slopes is not None:
+        _want(d_slopes, torch.float32, (plan.heads,), "d_slopes")
+    _check(_lib.attn_backward_mod(plan.handle, mod._for(plan), _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(o_t), _ptr(do_t),
+                                  _ptr(lse_t), _ptr(idx), _ptr(cnt), _ptr(dq_t), _ptr(dk_t), _ptr(dv_t),
+                                  _ptr(d_slopes), *_ws(ws), _stream(stream)), "attn_backward_mod")
+
+
+def attn_layer_mod(plan: Plan, rope, mod, q_nat, k_nat, v_nat, o_nat, ws, lse_nat=None, idx=None, cnt=None,
+                   stream=None):
+    """attn_layer with rotary positions (`rope`, may be None) and score rules (`mod`, may be None)."""
+    for name, t in (("q_nat", q_nat), ("k_nat", k_nat), ("v_nat", v_nat), ("o_nat", o_nat)):
+        _want(t, torch.bfloat16, plan.natural_shape(), name)
+    if lse_nat is not None:
+        _want(lse_nat, torch.float32, (plan.B, plan.heads, plan.L), "lse_nat")
+    if idx is not None:
+        _want_lists(plan, idx, cnt)
+    _check(_lib.attn_layer_mod(plan.handle, None if rope is None else rope._for(plan),
+                               None if mod is None else mod._for(plan), _ptr(q_nat), _ptr(k_nat), _ptr(v_nat),
+                               _ptr(o_nat), _ptr(lse_nat), _ptr(idx), _ptr(cnt), *_ws(ws), _stream(stream)),
+           "attn_layer_mod")
 
 
 def attn_check_device_status(plan: Plan, stream=None) -> int:

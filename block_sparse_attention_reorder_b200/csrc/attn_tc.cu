@@ -34,8 +34,10 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <type_traits>
 
 #include "internal.h"
+#include "score_mod.cuh"
 #include "tc_common.cuh"
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no
@@ -96,7 +98,12 @@ struct TcParams {
   int stall;             // testing: the MMA thread first waits on a barrier nothing arrives at
 };
 
-template <int D, bool FP8>
+struct TcParamsMod : TcParams {
+  ModParams mod;
+  float scale;
+};
+
+template <int D, bool FP8, bool MOD>
 struct Cfg {
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int QRB = D * ESZ;                 // Q/K row bytes
@@ -119,7 +126,9 @@ struct Cfg {
   static constexpr int OFF_COL = OFF_MISC + 16;         // 64 packed column coords
   static constexpr int OFF_SCAN = OFF_COL + 256;        // block-scan scratch
   static constexpr int OFF_TOK = OFF_SCAN + 64;         // epilogue: natural token of each block row
-  static constexpr int OFF_DYN = OFF_TOK + 512;         // bitmaps, union list
+  static constexpr int OFF_TAB = OFF_TOK + 512;         // score rules: a chunk's row offsets
+  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(mod::ColTab) : 0);  // bitmaps, union list
+  static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
   static constexpr int O_PITCH = D * 2 + 16;            // epilogue staging row pitch
   static_assert(OFF_Q % 1024 == 0 && OFF_K % 1024 == 0 && OFF_V % 1024 == 0, "alignment");
   static_assert(128 * O_PITCH <= OFF_BAR - OFF_K, "epilogue staging fits in the ring");
@@ -141,11 +150,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi, float& sum) 
 // layout [B, L, Hh, D] directly (else all tiled). Natural reads go
 // through five-dimensional tensor maps whose box is one tile. e4m3 Q/K are
 // always tile codes (tiled layout).
-template <int D, bool FP8, bool NAT>
+// MOD: score rules (score_mod.cuh) on the scores between the S product and
+// the softmax. The step list is filtered by them at set-up, so that chunks
+// hidden from the whole block cost nothing; of the rest only steps that need
+// element masks evaluate them. uext then holds packed coordinates and flags.
+template <int D, bool FP8, bool NAT, bool MOD>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, TcParams P) {
-  using C = Cfg<D, FP8>;
+               const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ std::conditional_t<MOD, TcParamsMod, TcParams> P) {
+  using C = Cfg<D, FP8, MOD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -166,6 +180,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   volatile int* never = reinterpret_cast<volatile int*>(misc + 3);  // stays 0: waits that ignore abort
   uint32_t* colc = reinterpret_cast<uint32_t*>(smem + C::OFF_COL);
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  mod::ColTab* coltab = reinterpret_cast<mod::ColTab*>(smem + C::OFF_TAB);  // score rules only
   uint32_t* bmA = reinterpret_cast<uint32_t*>(smem + C::OFF_DYN);
   uint32_t* bmB = bmA + P.bm_words;
   uint32_t* ulist = bmB + P.bm_words;
@@ -288,6 +303,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     tc::tmem_relinquish();
   }
   if (tid < 64) colc[tid] = chunk_row_code(g, tid);  // in-chunk (t, h, w) offsets of each chunk row
+  int prefix = 0;
+  if constexpr (MOD) {
+    if (tid < 64) mod::fill_coltab(g, coltab, tid);
+    if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
+  }
   if (g.cr < 64) {
     // Tiles of fewer than 64 tokens: natural-layout loads fill only the
     // chunk box's rows; the rest of every V slot must hold finite values.
@@ -390,6 +410,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
     }
     if (tid == 0) misc[2] = (uint32_t)min(tot, P.umax);
+  }
+  if constexpr (MOD) {
+    __syncthreads();
+    const int steps = (int)misc[2];
+    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext,
+                                                        nchunk > 1 ? uorg : nullptr, steps, scan);
+    __syncthreads();
+    if (tid == 0) misc[2] = (uint32_t)left;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -542,7 +570,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const bool row_exists = half == 0 || has1;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const float qsc = (FP8 && row_exists) ? P.qs[bh * g.N + (half ? i1 : i0)] : 1.f;
-    if (nchunk == 1 || FP8) {
+    if ((nchunk == 1 && !MOD) || FP8) {
       // Extents of one-chunk tiles, spread over the softmax threads (the
       // compaction above leaves them out: a dense bitmap word would put up
       // to 32 entries' divisions on one thread ahead of the CTA barrier),
@@ -550,13 +578,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // at once rather than one global load per step on the critical path.
       for (int n = r; n < L; n += 128) {
         const int jn = (int)(ulist[n] & 0x1FFFFFu);
-        if (nchunk == 1) uext[n] = chunk_ext(jn, ChunkOrigin{0, 0, 0});
+        if (nchunk == 1 && !MOD) uext[n] = chunk_ext(jn, ChunkOrigin{0, 0, 0});
         if (FP8) uks[n] = __ldg(P.ks + bh * g.N + jn);
       }
       asm volatile("bar.sync 2, 128;" ::: "memory");
     }
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    mod::Row row{};
+    float slope = 0.f;
+    if constexpr (MOD) {
+      if (row_exists) row = mod::row_of(g, P.mod, b, half ? i1 : i0, half ? c1 : c0, colc[r & 63], r & 63);
+      if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
+    }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
       const bool keep = ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
@@ -569,13 +603,57 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       uint32_t pk[32];
       bool need = false;
       float alpha = 1.f;
+      if constexpr (MOD) {
+        if ((uext[n] & mod::kHidden) && warp < 2) {
+          // V rows of hidden tokens become zeros before the product reads them.
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_vfull(n % kStages), (n / kStages) & 1, abort_flag, P.wait_limit))) {
+            ok = false;
+            break;
+          }
+          const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+          if (__ldg(P.mod.doc_rows + first + r) < 0) mod::zero_row(smem + C::OFF_V + (n % kStages) * C::V_BYTES, C::VBLK, r);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
       if (keep) {
         uint32_t sr[64];
         tc::tmem_ld64_wait(sbuf, sr);
-        const float c = P.scale_log2 * (FP8 ? qsc * uks[n] : 1.f);
+        float c = P.scale_log2 * (FP8 ? qsc * uks[n] : 1.f);
         const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
-        if (edge) {  // padded keys of an edge chunk
+        if constexpr (MOD) {
+          // Scores stay in units of `unit`: the raw products (unit = the
+          // scale), or tanh values (unit = the cap); the bias is added in the
+          // same units, and one FMA per score applies c = unit log2(e) as
+          // without rules.
+          const ModParams& M = P.mod;
+          float unit = P.scale * (FP8 ? qsc * uks[n] : 1.f);
+          if (M.cap > 0.f) {
+            mod::tanh_scores<64>(sr, unit / M.cap);
+            unit = M.cap;
+          }
+          c = unit * mod::kLog2e;
+          const mod::Coord f = mod::chunk_first(g, M, ext, step_origin(n));
+          if (M.slopes) {
+            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
+            const float per = -slope / unit;
+            const float nw[3] = {per * M.dist[0], per * M.dist[1], per * M.dist[2]};
+            mod::add_distance<64>(reinterpret_cast<float*>(sr), coltab, 0, at, nw);
+          }
+          if (ext & (mod::kEdge | mod::kCausal | mod::kDoc)) {
+            int vt = g.T - f.t;
+            if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
+            const int32_t* docs = nullptr;
+            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+#pragma unroll
+            for (int hq = 0; hq < 64; hq += 32) {
+              const uint32_t vis = mod::visible32(colc, hq, 0, vt, g.H - f.h, g.W - f.w, docs, row.id);
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (!((vis >> q) & 1u)) sr[hq + q] = 0xff800000u;  // -inf
+            }
+          }
+        } else if (edge) {  // padded keys of an edge chunk
           const int vt = (int)(ext & 0xffu), vh = (int)((ext >> 8) & 0xffu), vw = (int)((ext >> 16) & 0xffu);
 #pragma unroll
           for (int q = 0; q < 64; ++q) {
@@ -593,7 +671,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         const float m_new = fmaxf(m, mx);
         if (m == -INFINITY) {
-          m = m_new;  // first kept tile of this row: O row is still zero
+          m = m_new;  // first kept tile of this row (with rules: that shows it a key): O row is still zero
         } else if (m_new - m > kRescaleThreshold) {
           alpha = tc::ex2(m - m_new);
           m = m_new;
@@ -605,7 +683,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // CTAs' softmax warps, is not the bottleneck; edge tiles (with -inf
         // for padded keys) use the SFU throughout. The row sum uses the fp32
         // values, four packed chains.
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(-m, -m);
+        // A row that has seen no key yet has m = -inf and only -inf scores.
+        const float ms = MOD && m == -INFINITY ? 0.f : m;
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-ms, -ms);
         float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
         auto emit = [&](int q, float2 pv) {
@@ -613,7 +693,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           __nv_bfloat162 hv = __floats2bfloat162_rn(pv.x, pv.y);
           pk[q] = *reinterpret_cast<uint32_t*>(&hv);
         };
-        if (edge) {
+        if (MOD || edge) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1])), c2, nm2);
@@ -664,6 +744,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       tc::fence_after_sync();
     }
+    if constexpr (MOD) {
+      if (!row.live) l = 0.f;  // padded or hidden: a zero row
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
 #pragma unroll
@@ -674,6 +757,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       } else {
 #pragma unroll
         for (int q = 0; q < 32; ++q) o[q] = 0u;
+      }
+      if constexpr (MOD) {
+        if (!row.live) {  // whatever the row holds, NaN included
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0u;
+        }
       }
       uint32_t w[16];
       float dummy = 0.f;
@@ -753,10 +842,10 @@ bool make_map_nat(CUtensorMap* map, const void* base, const bsattn_plan* p) {
   return r == CUDA_SUCCESS;
 }
 
-template <int D, bool FP8, bool NAT>
+template <int D, bool FP8, bool NAT, bool MOD>
 bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v,
-                  TcParams prm, cudaStream_t st) {
-  using C = Cfg<D, FP8>;
+                  const std::conditional_t<MOD, TcParamsMod, TcParams>& prm, cudaStream_t st) {
+  using C = Cfg<D, FP8, MOD>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
@@ -774,7 +863,7 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
                 (FP8 ? (size_t)prm.umax * 4 : 0);
   if (smem < 80 * 1024) smem = 80 * 1024;  // at most two CTAs (2 x 256 TMEM columns) per SM
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = attn_tc_kernel<D, FP8, NAT>;
+  auto kern = attn_tc_kernel<D, FP8, NAT, MOD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -790,9 +879,9 @@ size_t attention_workspace_bytes(const bsattn_plan*) { return 0; }
 bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* k, const float* qs,
                                const float* ks, const __nv_bfloat16* v, const int32_t* idx,
                                const int32_t* cnt, __nv_bfloat16* o, float* lse, void*, size_t,
-                               cudaStream_t st, AttnLayout lay) {
+                               cudaStream_t st, AttnLayout lay, const ModParams* mod) {
   if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
-  TcParams prm;
+  TcParamsMod prm;
   prm.g = make_geom(p);
   prm.qs = qs;
   prm.ks = ks;
@@ -814,10 +903,18 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
   const int nd[3] = {p->nT, p->nH, p->nW};
   for (int a = 0; a < 3; ++a) prm.pdim[a] = a == prm.pair_axis ? (nd[a] + 1) / 2 : nd[a];
   const bool fp8 = p->desc.qk_fp8 != 0, d128 = p->desc.head_dim == 128;
-#define BSATTN_RUN(NATV)                                                                            \
-  return d128 ? (fp8 ? run<128, true, NATV>(p, q, k, v, prm, st) : run<128, false, NATV>(p, q, k, v, prm, st)) \
-              : (fp8 ? run<64, true, NATV>(p, q, k, v, prm, st) : run<64, false, NATV>(p, q, k, v, prm, st))
-  if (lay == AttnLayout::Natural) BSATTN_RUN(true);
-  BSATTN_RUN(false);
+  if (mod) {
+    prm.mod = *mod;
+    prm.scale = p->scale;
+  }
+#define BSATTN_RUN(NATV, MODV)                                                                                        \
+  return d128 ? (fp8 ? run<128, true, NATV, MODV>(p, q, k, v, prm, st) : run<128, false, NATV, MODV>(p, q, k, v, prm, st)) \
+              : (fp8 ? run<64, true, NATV, MODV>(p, q, k, v, prm, st) : run<64, false, NATV, MODV>(p, q, k, v, prm, st))
+  if (mod) {
+    if (lay == AttnLayout::Natural) BSATTN_RUN(true, true);
+    BSATTN_RUN(false, true);
+  }
+  if (lay == AttnLayout::Natural) BSATTN_RUN(true, false);
+  BSATTN_RUN(false, false);
 #undef BSATTN_RUN
 }

@@ -30,9 +30,18 @@
 // dQ [256, 256+D). Every mbarrier wait is bounded; on expiry the CTA sets
 // the device error word, raises an abort flag, lets issued copies land,
 // drains its MMAs and frees TMEM.
+//
+// Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased
+// and masked scores; the step lists are filtered as in the forward. Hidden
+// pairs take no part through selects (their scores may be NaN), and the rows
+// of hidden tokens in a step's tiles are zeroed in shared memory before the
+// product that sums over them.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "internal.h"
+#include "score_mod.cuh"
 #include "tc_common.cuh"
 
 namespace {
@@ -43,6 +52,25 @@ constexpr int kStages = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
+
+// Score rules: a chunk's row offsets, and every chunk's in-tile origin
+// (packed 10 bits per axis), so that a step needs no division.
+struct ModTab {
+  mod::ColTab col;
+  uint32_t origin[kMaxChunks];
+  __device__ __forceinline__ ChunkOrigin at(int c) const {
+    const uint32_t v = origin[c];
+    return ChunkOrigin{(int)(v & 0x3FFu), (int)((v >> 10) & 0x3FFu), (int)(v >> 20)};
+  }
+};
+template <int NT>
+__device__ __forceinline__ void fill_modtab(const Geom& g, ModTab* tab) {
+  if (threadIdx.x < 64) mod::fill_coltab(g, &tab->col, threadIdx.x);
+  for (int c = threadIdx.x; c < g.nchunk; c += NT) {
+    const ChunkOrigin o = chunk_origin(g, c);
+    tab->origin[c] = (uint32_t)o.dt | ((uint32_t)o.dh << 10) | ((uint32_t)o.dw << 20);
+  }
+}
 
 struct DqParams {
   Geom g;
@@ -61,7 +89,12 @@ struct DqParams {
   int pdim[3];
 };
 
-template <int D>
+struct DqParamsMod : DqParams {
+  ModParams mod;
+  float* slope_parts;  // null, or [B * heads, CTAs per head]: the slope gradient's parts
+};
+
+template <int D, bool MOD>
 struct DqCfg {
   static constexpr int QRB = D * 2;                  // row bytes
   static constexpr int QBLK = QRB / 128;             // 128-byte column blocks
@@ -78,7 +111,9 @@ struct DqCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort, L, zero
   static constexpr int OFF_COL = OFF_MISC + 16;        // 64 packed in-tile coordinates
   static constexpr int OFF_SCAN = OFF_COL + 256;
-  static constexpr int OFF_DYN = OFF_SCAN + 64;        // bitmaps, step list, extents
+  static constexpr int OFF_TAB = OFF_SCAN + 64;        // score rules: row offsets, chunk origins
+  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(ModTab) : 0);  // bitmaps, step list, extents
+  static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
   static constexpr int O_PITCH = D * 2 + 16;           // epilogue staging pitch
   static_assert(128 * O_PITCH <= OFF_BAR - OFF_K, "epilogue staging fits in the rings");
 };
@@ -183,11 +218,12 @@ __device__ __forceinline__ void compact_steps(const Geom& g, const uint32_t* bmA
   if (tid == 0) *count = (uint32_t)min(tot, cap);
 }
 
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
-                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, DqParams P) {
-  using C = DqCfg<D>;
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ std::conditional_t<MOD, DqParamsMod, DqParams> P) {
+  using C = DqCfg<D, MOD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -239,6 +275,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc::tmem_relinquish();
   }
   if (tid < 64) colc[tid] = chunk_row_code(g, tid);  // in-chunk (t, h, w) offsets of each chunk row
+  ModTab* tab = reinterpret_cast<ModTab*>(smem + C::OFF_TAB);  // score rules only
+  int prefix = 0;
+  if constexpr (MOD) {
+    fill_modtab<kThreads>(g, tab);
+    if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
+  }
   for (int w = tid; w < 2 * P.bm_words; w += kThreads) bmA[w] = 0u;
   if (!has1) {  // rows 64..127 have no tile: zero their Q and dO
     for (int x = tid; x < C::QBLK * 64 * 128 / 16; x += kThreads) {
@@ -276,6 +318,13 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
   __syncthreads();
   compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
+  if constexpr (MOD) {
+    __syncthreads();
+    const int steps = (int)misc[2];
+    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, nullptr, steps, scan);
+    __syncthreads();
+    if (tid == 0) misc[2] = (uint32_t)left;
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -390,6 +439,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const float dlt = row_exists ? P.delta[lrow] : 0.f;
     const float c = P.scale_log2;
     bool ok = true;
+    mod::Row row{};
+    float slope = 0.f, sw = 0.f, swd = 0.f, spd = 0.f;  // sums of w = P (dP - Delta), w dist, P dist
+    if constexpr (MOD) {
+      if (row_exists) row = mod::row_of(g, P.mod, b, half ? i1 : i0, half ? c1 : c0, colc[r & 63], r & 63);
+      if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
+    }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
       const bool keep = row_exists && ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
@@ -401,7 +456,68 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint32_t sbuf = tmem + lane_base + kColS + (n & 1) * 64 + 32 * part;
       const uint32_t pbuf = tmem + lane_base + kColDP + (n & 1) * 64 + 32 * part;
       uint32_t dsw[16];
-      if (keep) {
+      if constexpr (MOD) {
+        if ((uext[n] & mod::kHidden) && tid < 64) {  // K rows of hidden tokens (S has been formed)
+          const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+          if (__ldg(P.mod.doc_rows + first + tid) < 0)
+            mod::zero_row(smem + C::OFF_K + (n % kStages) * C::T_BYTES, C::QBLK, tid);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
+      if (MOD && keep) {
+        if constexpr (MOD) {
+          const ModParams& M = P.mod;
+          const uint32_t ext = uext[n];
+          const ChunkOrigin org = tab->at((int)((e >> 21) & 0x1FFu));
+          const mod::Coord f = mod::chunk_first(g, M, ext, org);
+          uint32_t vis = row.live ? 0xffffffffu : 0u;
+          if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
+            int vt = g.T - f.t;
+            if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
+            const int32_t* docs = nullptr;
+            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+            vis = mod::visible32(colc, 32 * part, 0, vt, g.H - f.h, g.W - f.w, docs, row.id);
+          }
+          uint32_t sr[32], pr[32];
+          tc::tmem_ld32_wait(sbuf, sr);
+          tc::tmem_ld32_wait(pbuf, pr);
+          // y = log2 of P: raw scores (or tanh values) times c2, bias, minus the log-sum-exp.
+          float c2 = c;
+          const bool cap = M.cap > 0.f;
+          if (cap) {
+            mod::tanh_scores<32>(sr, P.scale / M.cap);
+            c2 = M.cap * mod::kLog2e;
+          }
+          float far[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) far[q] = 0.f;
+          if (M.slopes) {
+            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
+            mod::add_distance<32>(far, &tab->col, 32 * part, at, M.dist);
+          }
+          const float s2 = -slope * mod::kLog2e;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float d2[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int x = 2 * q + u;
+              const float th = __uint_as_float(sr[x]);
+              const bool see = (vis >> x) & 1u;
+              const float p = see ? tc::ex2(fmaf(far[x], s2, fmaf(th, c2, -lse2))) : 0.f;
+              const float w = see ? p * (__uint_as_float(pr[x]) - dlt) : 0.f;
+              if (P.slope_parts) {
+                sw += w;
+                swd = fmaf(w, far[x], swd);
+                spd = fmaf(p, far[x], spd);
+              }
+              d2[u] = cap ? (see ? w * fmaf(-th, th, 1.f) : 0.f) : w;
+            }
+            __nv_bfloat162 hv = __floats2bfloat162_rn(d2[0], d2[1]);
+            dsw[q] = *reinterpret_cast<uint32_t*>(&hv);
+          }
+        }
+      } else if (!MOD && keep) {
         const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
         const int vt = (int)(ext & 0xffu), vh = (int)((ext >> 8) & 0xffu), vw = (int)((ext >> 16) & 0xffu);
@@ -446,6 +562,32 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       tc::fence_after_sync();
     }
+    if constexpr (MOD) {
+      if (P.slope_parts) {
+        // Row r's share of -sum dZ dist. With w = P (dP - Delta) for any Delta
+        // and sum P = 1, dZ = w - P sum w: the rounding of O in Delta drops out.
+        float* red = reinterpret_cast<float*>(smem + C::OFF_V);  // the V ring is no longer read
+        const bool use = ok && L > 0;
+        if (use) {
+          red[3 * tid] = sw;
+          red[3 * tid + 1] = swd;
+          red[3 * tid + 2] = spd;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+        float v = 0.f;
+        if (use && part == 0 && row.live) {
+          const int o = 3 * (tid + 128);
+          v = (sw + red[o]) * (spd + red[o + 2]) - (swd + red[o + 1]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (part == 0 && lane == 0) scan[warp] = __float_as_int(v);
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+        if (tid == 0)
+          P.slope_parts[bh * gridDim.x + blockIdx.x] = (__int_as_float(scan[0]) + __int_as_float(scan[1])) +
+                                                       (__int_as_float(scan[2]) + __int_as_float(scan[3]));
+      }
+    }
     uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
     constexpr int OC = D / 2;  // dQ columns this warp writes
 #pragma unroll
@@ -456,6 +598,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       } else {
 #pragma unroll
         for (int q = 0; q < 32; ++q) o[q] = 0u;
+      }
+      if constexpr (MOD) {
+        if (!row.live) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0u;
+        }
       }
       uint32_t w[16];
 #pragma unroll
@@ -488,10 +636,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-template <int D>
+template <int D, bool MOD>
 bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* d_o,
-                     DqParams prm, cudaStream_t st) {
-  using C = DqCfg<D>;
+                     const std::conditional_t<MOD, DqParamsMod, DqParams>& prm, cudaStream_t st) {
+  using C = DqCfg<D, MOD>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mdo, mk, mv;
@@ -503,7 +651,7 @@ bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const v
     return BSATTN_ERR_CUDA;
   const size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = bwd_dq_tc_kernel<D>;
+  auto kern = bwd_dq_tc_kernel<D, MOD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -541,7 +689,11 @@ struct KvParams {
   int pdim[3];
 };
 
-template <int D>
+struct KvParamsMod : KvParams {
+  ModParams mod;
+};
+
+template <int D, bool MOD>
 struct KvCfg {
   static constexpr int QRB = D * 2;
   static constexpr int QBLK = QRB / 128;
@@ -557,17 +709,20 @@ struct KvCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_COL = OFF_MISC + 16;
   static constexpr int OFF_SCAN = OFF_COL + 256;
-  static constexpr int OFF_DYN = OFF_SCAN + 64;
+  static constexpr int OFF_TAB = OFF_SCAN + 64;
+  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(ModTab) : 0);
+  static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
   static constexpr int O_PITCH = D * 2 + 16;
   static_assert(STAGE % 1024 == 0, "stage alignment");
   static_assert(2 * 128 * O_PITCH <= OFF_BAR - OFF_RING, "epilogue staging fits in the ring");
 };
 
-template <int D>
+template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
-                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, KvParams P) {
-  using C = KvCfg<D>;
+                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ std::conditional_t<MOD, KvParamsMod, KvParams> P) {
+  using C = KvCfg<D, MOD>;
   constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 256 + D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -628,6 +783,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tc::tmem_relinquish();
   }
   if (tid < 64) colc[tid] = chunk_row_code(g, tid);  // in-chunk (t, h, w) offsets of each chunk row
+  ModTab* tab = reinterpret_cast<ModTab*>(smem + C::OFF_TAB);  // score rules only
+  int prefix = 0;
+  if constexpr (MOD) {
+    fill_modtab<kThreads>(g, tab);
+    if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
+  }
   for (int w = tid; w < 2 * P.bm_words; w += kThreads) bmA[w] = 0u;
   if (!has1) {  // rows 64..127 have no key tile: zero their K and V
     for (int x = tid; x < C::QBLK * 64 * 128 / 16; x += kThreads) {
@@ -656,6 +817,13 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   }
   __syncthreads();
   compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
+  if constexpr (MOD) {
+    __syncthreads();
+    const int steps = (int)misc[2];
+    const int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, nullptr, steps, scan);
+    __syncthreads();
+    if (tid == 0) misc[2] = (uint32_t)left;
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -775,6 +943,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float c = P.scale_log2;
     bool ok = true;
+    mod::Row row{};
+    float slope = 0.f;
+    if constexpr (MOD) {
+      if (row_exists) row = mod::row_of(g, P.mod, b, half ? j1 : j0, half ? kc1 : kc0, colc[r & 63], r & 63);
+      if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
+    }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
       const bool keep = row_exists && ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
@@ -792,7 +966,68 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         break;
       }
       uint32_t pw[16], dw[16];
-      if (keep) {
+      if constexpr (MOD) {
+        if ((uext[n] & mod::kHidden) && tid < 64) {  // Q and dO rows of hidden tokens (S and dP have been formed)
+          const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+          if (__ldg(P.mod.doc_rows + first + tid) < 0) {
+            uint8_t* tile = smem + C::OFF_RING + (n % kStages) * C::STAGE;
+            mod::zero_row(tile, C::QBLK, tid);
+            mod::zero_row(tile + C::T_BYTES, C::QBLK, tid);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
+      if (MOD && keep) {
+        if constexpr (MOD) {
+          const ModParams& M = P.mod;
+          const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
+          const uint32_t ext = uext[n];
+          const ChunkOrigin org = tab->at((int)((e >> 21) & 0x1FFu));
+          const mod::Coord f = mod::chunk_first(g, M, ext, org);
+          uint32_t vis = row.live ? 0xffffffffu : 0u;
+          if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
+            // Queries at or behind the key's frame, all of them for a key of the prefix.
+            const int lo = M.causal && row.at.t >= prefix ? row.at.t - f.t : 0;
+            const int32_t* docs = nullptr;
+            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+            vis = mod::visible32(colc, 32 * part, lo, g.T - f.t, g.H - f.h, g.W - f.w, docs, row.id);
+          }
+          uint32_t sr[32], pr[32];
+          tc::tmem_ld32_wait(sbuf, sr);
+          tc::tmem_ld32_wait(pbuf, pr);
+          float c2 = c;
+          const bool cap = M.cap > 0.f;
+          if (cap) {
+            mod::tanh_scores<32>(sr, P.scale / M.cap);
+            c2 = M.cap * mod::kLog2e;
+          }
+          float y[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) y[q] = fmaf(__uint_as_float(sr[q]), c2, -ld[32 * part + q] * mod::kLog2e);
+          if (M.slopes) {
+            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
+            const float s2 = -slope * mod::kLog2e;
+            const float nw[3] = {s2 * M.dist[0], s2 * M.dist[1], s2 * M.dist[2]};
+            mod::add_distance<32>(y, &tab->col, 32 * part, at, nw);
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float pp[2], d2[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int x = 2 * q + u;
+              const float th = __uint_as_float(sr[x]);
+              const bool see = (vis >> x) & 1u;
+              pp[u] = see ? tc::ex2(y[x]) : 0.f;
+              const float w = pp[u] * (__uint_as_float(pr[x]) - ld[64 + 32 * part + x]);
+              d2[u] = see ? (cap ? w * fmaf(-th, th, 1.f) : w) : 0.f;
+            }
+            __nv_bfloat162 hp = __floats2bfloat162_rn(pp[0], pp[1]), hd = __floats2bfloat162_rn(d2[0], d2[1]);
+            pw[q] = *reinterpret_cast<uint32_t*>(&hp);
+            dw[q] = *reinterpret_cast<uint32_t*>(&hd);
+          }
+        }
+      } else if (!MOD && keep) {
         const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
         const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
@@ -858,6 +1093,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = 0u;
         }
+        if constexpr (MOD) {
+          if (!row.live) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = 0u;
+          }
+        }
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -891,10 +1132,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   }
 }
 
-template <int D>
+template <int D, bool MOD>
 bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* d_o,
-                       KvParams prm, cudaStream_t st) {
-  using C = KvCfg<D>;
+                       const std::conditional_t<MOD, KvParamsMod, KvParams>& prm, cudaStream_t st) {
+  using C = KvCfg<D, MOD>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mdo, mk, mv;
@@ -906,7 +1147,7 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
     return BSATTN_ERR_CUDA;
   const size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = bwd_dkdv_tc_kernel<D>;
+  auto kern = bwd_dkdv_tc_kernel<D, MOD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -919,8 +1160,9 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
 
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, const float* delta, const int32_t* idx,
-                                    const int32_t* cnt, void* dq, cudaStream_t st) {
-  DqParams prm;
+                                    const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod,
+                                    float* slope_parts) {
+  DqParamsMod prm;
   prm.g = make_geom(p);
   prm.idx = idx;
   prm.cnt = cnt;
@@ -937,13 +1179,20 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
   prm.pair_axis = pair_axis_of(p);
   const int nd[3] = {p->nT, p->nH, p->nW};
   for (int a = 0; a < 3; ++a) prm.pdim[a] = a == prm.pair_axis ? (nd[a] + 1) / 2 : nd[a];
-  return p->desc.head_dim == 128 ? run_dq<128>(p, q, k, v, d_o, prm, st) : run_dq<64>(p, q, k, v, d_o, prm, st);
+  const bool d128 = p->desc.head_dim == 128;
+  if (mod) {
+    prm.mod = *mod;
+    prm.slope_parts = slope_parts;
+    return d128 ? run_dq<128, true>(p, q, k, v, d_o, prm, st) : run_dq<64, true>(p, q, k, v, d_o, prm, st);
+  }
+  return d128 ? run_dq<128, false>(p, q, k, v, d_o, prm, st) : run_dq<64, false>(p, q, k, v, d_o, prm, st);
 }
 
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                       const void* d_o, const float* lse, const float* delta, const int32_t* idxT,
-                                      const int32_t* cntT, void* dk, void* dv, cudaStream_t st) {
-  KvParams prm;
+                                      const int32_t* cntT, void* dk, void* dv, cudaStream_t st,
+                                      const ModParams* mod) {
+  KvParamsMod prm;
   prm.g = make_geom(p);
   prm.idxT = idxT;
   prm.cntT = cntT;
@@ -960,6 +1209,10 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
   prm.pair_axis = pair_axis_of(p);
   const int nd[3] = {p->nT, p->nH, p->nW};
   for (int a = 0; a < 3; ++a) prm.pdim[a] = a == prm.pair_axis ? (nd[a] + 1) / 2 : nd[a];
-  return p->desc.head_dim == 128 ? run_dkdv<128>(p, q, k, v, d_o, prm, st)
-                                 : run_dkdv<64>(p, q, k, v, d_o, prm, st);
+  const bool d128 = p->desc.head_dim == 128;
+  if (mod) {
+    prm.mod = *mod;
+    return d128 ? run_dkdv<128, true>(p, q, k, v, d_o, prm, st) : run_dkdv<64, true>(p, q, k, v, d_o, prm, st);
+  }
+  return d128 ? run_dkdv<128, false>(p, q, k, v, d_o, prm, st) : run_dkdv<64, false>(p, q, k, v, d_o, prm, st);
 }

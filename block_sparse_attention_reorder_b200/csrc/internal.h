@@ -152,6 +152,19 @@ bsattn_status launch_select_topp(int rows, int N, int k, double p, const float* 
 bsattn_status launch_broadcast_lists(int bh, int N, int kmax, const int32_t* src_idx,
                                      const int32_t* src_cnt, int32_t* idx, int32_t* cnt,
                                      cudaStream_t st);
+// Score rules of one call on the device (attn_*_mod). doc_rows and doc_chunks
+// live in the call's workspace.
+struct ModParams {
+  float cap;                 // 0: off
+  const float* slopes;       // null: no bias
+  float dist[3];
+  int causal;
+  const int32_t* prefix;     // null: 0
+  const int32_t* doc_rows;   // null: no documents; [B, N, V] ids in tile order, padded slots -1
+  const int4* doc_chunks;    // [B, N, nchunk] (least, greatest id >= 0, tokens with one, tokens without)
+  int sh_h, sh_w;            // bits of a tile's h and w coordinates (packed step coordinates)
+};
+
 // Where the attention's tensors live. Tiled: all tiled. Natural: Q, K, V, O
 // and lse in the natural layout ([B, L, Hh, D], [B, Hh, L]). e4m3 Q/K are
 // tile codes in both layouts.
@@ -160,7 +173,7 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
                                const float* qs, const float* ks, const __nv_bfloat16* v,
                                const int32_t* idx, const int32_t* cnt, __nv_bfloat16* o,
                                float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
-                               AttnLayout lay);
+                               AttnLayout lay, const ModParams* mod = nullptr);
 // Tile axis (0 = t, 1 = h, 2 = w) along which two 64-token tiles are stacked
 // into one 128-row block (attention: query tiles; dK/dV: key tiles). Top-k and
 // top-p: t, whose neighbouring tiles keep the most key tiles in common on the
@@ -185,18 +198,35 @@ struct BackwardWs {
 };
 bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* o,
                               const void* d_o, const float* lse, const int32_t* idx, const int32_t* cnt, void* dq,
-                              void* dk, void* dv, const BackwardWs& w, cudaStream_t st);
+                              void* dk, void* dv, const BackwardWs& w, cudaStream_t st,
+                              const ModParams* mod = nullptr, float* slope_parts = nullptr);
 
 // dQ of the backward on the tensor cores (tiled bf16 q, k, v, dO; lse and
 // rowsum(dO * O) tiled fp32).
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, const float* delta, const int32_t* idx,
-                                    const int32_t* cnt, void* dq, cudaStream_t st);
+                                    const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod = nullptr,
+                                    float* slope_parts = nullptr);
 
 // dK and dV of the backward on the tensor cores, over the transposed lists.
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                       const void* d_o, const float* lse, const float* delta, const int32_t* idxT,
-                                      const int32_t* cntT, void* dk, void* dv, cudaStream_t st);
+                                      const int32_t* cntT, void* dk, void* dv, cudaStream_t st,
+                                      const ModParams* mod = nullptr);
+// CTAs of the attention kernels per (batch, head): 128-row query (key) blocks.
+static inline int attention_items(const bsattn_plan* p) {
+  if (p->nchunk > 1) return p->N * ((p->nchunk + 1) / 2);
+  const int nd[3] = {p->nT, p->nH, p->nW}, a = pair_axis_of(p);
+  return p->N / nd[a] * ((nd[a] + 1) / 2);
+}
+
+bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r);
+// Rotation of one or two natural tensors (r null: a copy), with fp32 tile means
+// where asked. doc, if given ([B, L]): tokens with a negative id are written as
+// zeros and left out of the means (0 for a tile of such tokens only).
+bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv_bfloat16* x0, __nv_bfloat16* y0,
+                          const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1, bool transpose,
+                          const int32_t* doc, cudaStream_t st);
 
 // 2-D tiled tensor map over `rows` rows of `inner` elements of `esz` bytes.
 bool bsattn_make_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esz, int inner,

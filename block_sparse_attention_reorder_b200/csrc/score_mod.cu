@@ -1,0 +1,428 @@
+// Score rules: their checks and entry points, document ids brought into tile
+// order, the rules on block scores, and the sum of the slope gradient's parts.
+// The rules inside the attention kernels are in score_mod.cuh.
+#include "score_mod.cuh"
+
+#include <float.h>
+#include <limits.h>
+
+namespace {
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+struct Carve {
+  uint8_t* base;
+  size_t off = 0;
+  explicit Carve(void* b) : base((uint8_t*)b) {}
+  void* take(size_t bytes) {
+    void* r = base ? base + off : nullptr;
+    off += align_up(bytes, 256);
+    return r;
+  }
+};
+
+// Ids in tile order, and their ranges per 64-row chunk and per tile.
+struct DocWs {
+  int32_t* rows;  // [B, N, V]
+  int4* chunks;   // [B, N, nchunk]
+  int2* tiles;    // [B, N] least and greatest id >= 0 (INT_MAX, -1: none)
+};
+
+DocWs carve_doc(const bsattn_plan* p, Carve& c) {
+  const size_t bn = (size_t)p->desc.B * p->N;
+  DocWs w;
+  w.rows = (int32_t*)c.take(bn * p->V * sizeof(int32_t));
+  w.chunks = (int4*)c.take(bn * p->nchunk * sizeof(int4));
+  w.tiles = (int2*)c.take(bn * sizeof(int2));
+  return w;
+}
+
+struct BwdModWs {
+  DocWs doc;
+  float* slope_parts;
+  BackwardWs b;
+};
+BwdModWs carve_backward_mod(const bsattn_plan* p, Carve& c) {
+  const size_t rows = (size_t)p->desc.B * p->desc.heads * p->N;
+  BwdModWs w;
+  w.doc = carve_doc(p, c);
+  w.slope_parts = (float*)c.take((size_t)p->desc.B * p->desc.heads * attention_items(p) * sizeof(float));
+  w.b.delta = (float*)c.take(rows * p->V * sizeof(float));
+  w.b.bm = (uint32_t*)c.take(rows * ((p->N + 31) / 32) * sizeof(uint32_t));
+  w.b.idxT = (int32_t*)c.take(rows * p->N * sizeof(int32_t));
+  w.b.cntT = (int32_t*)c.take(rows * sizeof(int32_t));
+  return w;
+}
+
+struct LayerModWs {
+  DocWs doc;
+  __nv_bfloat16 *q, *k;  // rotated
+  uint8_t *qc, *kc;      // e4m3 tile codes
+  float *qs, *ks;
+  float *pq, *pk, *S;
+  int32_t *idx, *cnt;
+};
+LayerModWs carve_layer_mod(const bsattn_plan* p, Carve& c) {
+  const size_t bh = (size_t)p->desc.B * p->desc.heads, D = p->desc.head_dim;
+  const bool route = p->rule.kind != BSATTN_RULE_WINDOW;
+  const size_t codes = p->desc.qk_fp8 ? bh * p->N * p->V * D : 0;
+  LayerModWs w;
+  w.doc = carve_doc(p, c);
+  w.q = (__nv_bfloat16*)c.take(bh * p->L * D * 2);
+  w.k = (__nv_bfloat16*)c.take(bh * p->L * D * 2);
+  w.qc = (uint8_t*)c.take(codes);
+  w.kc = (uint8_t*)c.take(codes);
+  w.qs = (float*)c.take(p->desc.qk_fp8 ? bh * p->N * sizeof(float) : 0);
+  w.ks = (float*)c.take(p->desc.qk_fp8 ? bh * p->N * sizeof(float) : 0);
+  w.pq = (float*)c.take(route ? bh * p->N * D * sizeof(float) : 0);
+  w.pk = (float*)c.take(route ? bh * p->N * D * sizeof(float) : 0);
+  w.S = (float*)c.take(route ? bh * p->N * p->N * sizeof(float) : 0);
+  w.idx = (int32_t*)c.take(bh * p->N * p->kmax * sizeof(int32_t));
+  w.cnt = (int32_t*)c.take(bh * p->N * sizeof(int32_t));
+  return w;
+}
+
+// One CTA of two warps per (tile, batch): the ids of the tile's rows, and
+// their ranges. A few bytes per token; bound by its launch.
+__global__ void __launch_bounds__(64) doc_prep_kernel(Geom g, const int32_t* __restrict__ doc, DocWs w) {
+  __shared__ int4 part[2];
+  const int j = blockIdx.x, b = blockIdx.y, r = threadIdx.x;
+  const int t0 = j / (g.nH * g.nW) * g.tt, h0 = j / g.nW % g.nH * g.th, w0 = j % g.nW * g.tw;
+  const uint32_t code = chunk_row_code(g, r);
+  int2 tile = make_int2(INT_MAX, -1);
+  for (int c = 0; c < g.nchunk; ++c) {
+    const ChunkOrigin o = chunk_origin(g, c);
+    const int t = t0 + o.dt + (int)(code & 0xffu), h = h0 + o.dh + (int)((code >> 8) & 0xffu),
+              x = w0 + o.dw + (int)((code >> 16) & 0xffu);
+    const bool real = r < g.cr && t < g.T && h < g.H && x < g.W;
+    const int id = real ? doc[(size_t)b * g.L + (t * g.H + h) * g.W + x] : -1;
+    w.rows[((size_t)b * g.N + j) * g.V + 64 * c + r] = id < 0 ? -1 : id;
+    int lo = id >= 0 ? id : INT_MAX, hi = id >= 0 ? id : -1, with = id >= 0, without = real && id < 0;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    with = __reduce_add_sync(0xffffffffu, with);
+    without = __reduce_add_sync(0xffffffffu, without);
+    if (r % 32 == 0) part[r / 32] = make_int4(lo, hi, with, without);
+    __syncthreads();
+    if (r == 0) {
+      const int4 p = part[0], q = part[1];
+      const int4 all = make_int4(min(p.x, q.x), max(p.y, q.y), p.z + q.z, p.w + q.w);
+      w.chunks[((size_t)b * g.N + j) * g.nchunk + c] = all;
+      tile = make_int2(min(tile.x, all.x), max(tile.y, all.y));
+    }
+    __syncthreads();
+  }
+  if (r == 0) w.tiles[(size_t)b * g.N + j] = tile;
+}
+
+// The rules on block scores, S' from S. Memory bound (8 bytes an entry): a
+// thread owns four neighbouring key tiles, whose mean coordinates and ranges
+// it keeps in registers (no division per entry), and walks kScoreRows query
+// tiles, whose own come from shared memory.
+constexpr int kScoreRows = 32;
+constexpr int kScoreThreads = 128;
+
+struct TileMeta {
+  float t, h, w;  // mean coordinates of the real tokens
+  int first, last;  // frames
+  int2 ids;
+};
+__device__ __forceinline__ TileMeta tile_meta(const Geom& g, int j, int b, const int2* ids) {
+  const int t0 = j / (g.nH * g.nW) * g.tt, h0 = j / g.nW % g.nH * g.th, w0 = j % g.nW * g.tw;
+  const int vt = min(g.tt, g.T - t0), vh = min(g.th, g.H - h0), vw = min(g.tw, g.W - w0);
+  TileMeta m{t0 + 0.5f * (vt - 1), h0 + 0.5f * (vh - 1), w0 + 0.5f * (vw - 1), t0, t0 + vt - 1, make_int2(0, 0)};
+  if (ids) m.ids = __ldg(ids + (size_t)b * g.N + j);
+  return m;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kScoreThreads)
+mod_scores_kernel(Geom g, ModParams m, const int2* __restrict__ ids, const float* S, float* out) {
+  __shared__ TileMeta rowm[kScoreRows];
+  const int N = g.N, bh = blockIdx.z, b = bh / g.Hh, head = bh % g.Hh;
+  const int i0 = blockIdx.y * kScoreRows, rows = min(kScoreRows, N - i0);
+  const int j0 = 4 * (blockIdx.x * kScoreThreads + threadIdx.x);
+  if (threadIdx.x < rows) rowm[threadIdx.x] = tile_meta(g, i0 + threadIdx.x, b, ids);
+  __syncthreads();
+  if (j0 >= N) return;
+  TileMeta km[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) km[e] = tile_meta(g, min(j0 + e, N - 1), b, ids);
+  const float slope = m.slopes ? __ldg(m.slopes + head) : 0.f;
+  const int prefix = m.prefix ? __ldg(m.prefix + b) : 0;
+  const float inv = m.cap > 0.f ? 1.f / m.cap : 0.f;
+  const float* src = S + ((size_t)bh * N + i0) * N + j0;
+  float* dst = out + ((size_t)bh * N + i0) * N + j0;
+  const int ne = min(4, N - j0);
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (VEC) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (size_t)i * N);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < ne) v[e] = src[(size_t)i * N + e];
+    }
+    const TileMeta q = rowm[i];
+    if (m.cap > 0.f) {
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float2 u = make_float2(v[e] * inv, v[e + 1] * inv);
+        const float2 t = mod::tanh_small2(u);
+        v[e] = m.cap * (fabsf(u.x) <= mod::kSmall ? t.x : mod::tanh_any(u.x));
+        v[e + 1] = m.cap * (fabsf(u.y) <= mod::kSmall ? t.y : mod::tanh_any(u.y));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (m.slopes) {
+        float far = m.dist[0] * fabsf(q.t - km[e].t);
+        far = fmaf(m.dist[1], fabsf(q.h - km[e].h), far);
+        far = fmaf(m.dist[2], fabsf(q.w - km[e].w), far);
+        v[e] = fmaf(-slope, far, v[e]);
+      }
+      bool hide = m.causal && km[e].first > q.last && km[e].first >= prefix;
+      if (ids) hide = hide || km[e].ids.x > q.ids.y || q.ids.x > km[e].ids.y;
+      if (hide) v[e] = -FLT_MAX;
+    }
+    if (VEC) {
+      *reinterpret_cast<float4*>(dst + (size_t)i * N) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < ne) dst[(size_t)i * N + e] = v[e];
+    }
+  }
+}
+
+// d_slopes[head] = sum of the head's parts over batches and CTAs, in a fixed
+// order in fp64.
+__global__ void __launch_bounds__(256) slope_sum_kernel(const float* __restrict__ parts, int B, int heads, int items,
+                                                        float* __restrict__ d_slopes) {
+  __shared__ double red[256];
+  const int head = blockIdx.x;
+  double s = 0.0;
+  for (int b = 0; b < B; ++b)
+    for (int x = threadIdx.x; x < items; x += 256) s += (double)parts[((size_t)b * heads + head) * items + x];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) d_slopes[head] = (float)red[0];
+}
+
+bool ok_ptr(const void* x) { return x != nullptr && aligned16(x); }
+
+bsattn_status check_mod(const bsattn_score_mod* m) {
+  if (!m) return BSATTN_ERR_INVALID_ARG;
+  if (!(m->softcap >= 0.f) || !isfinite(m->softcap)) return BSATTN_ERR_INVALID_ARG;
+  const float d[3] = {m->dist_t, m->dist_h, m->dist_w};
+  for (float x : d)
+    if (!(x >= 0.f) || !isfinite(x)) return BSATTN_ERR_INVALID_ARG;
+  if (m->causal != 0 && m->causal != 1) return BSATTN_ERR_INVALID_ARG;
+  if (m->prefix && !m->causal) return BSATTN_ERR_INVALID_ARG;
+  if (!aligned16(m->slopes) || !aligned16(m->prefix) || !aligned16(m->doc)) return BSATTN_ERR_INVALID_ARG;
+  return BSATTN_OK;
+}
+
+int bits_of(int n) {  // bits of 0 .. n - 1
+  int b = 0;
+  while ((1 << b) < n) ++b;
+  return b;
+}
+
+ModParams device_mod(const bsattn_plan* p, const bsattn_score_mod* m, const DocWs& w) {
+  ModParams d;
+  d.cap = m->softcap;
+  d.slopes = m->slopes;
+  d.dist[0] = m->dist_t; d.dist[1] = m->dist_h; d.dist[2] = m->dist_w;
+  d.causal = m->causal;
+  d.prefix = m->prefix;
+  d.doc_rows = m->doc ? w.rows : nullptr;
+  d.doc_chunks = m->doc ? w.chunks : nullptr;
+  d.sh_h = bits_of(p->nH);
+  d.sh_w = bits_of(p->nW);
+  return d;
+}
+
+bsattn_status launch_doc_prep(const bsattn_plan* p, const bsattn_score_mod* m, const DocWs& w, cudaStream_t st) {
+  if (!m->doc) return BSATTN_OK;
+  if (p->desc.B > 65535) return BSATTN_ERR_UNSUPPORTED;
+  doc_prep_kernel<<<dim3(p->N, p->desc.B), 64, 0, st>>>(make_geom(p), m->doc, w);
+  return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+bsattn_status launch_mod_scores(const bsattn_plan* p, const ModParams& d, const int2* ids, const float* S, float* out,
+                                cudaStream_t st) {
+  const Geom g = make_geom(p);
+  if ((long long)g.B * g.Hh > 65535) return BSATTN_ERR_UNSUPPORTED;
+  dim3 grid((g.N + 4 * kScoreThreads - 1) / (4 * kScoreThreads), (g.N + kScoreRows - 1) / kScoreRows, g.B * g.Hh);
+  if (g.N % 4 == 0)  // every row starts on 16 bytes
+    mod_scores_kernel<true><<<grid, kScoreThreads, 0, st>>>(g, d, ids, S, out);
+  else
+    mod_scores_kernel<false><<<grid, kScoreThreads, 0, st>>>(g, d, ids, S, out);
+  return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+// The workspace of calls that need one for documents only.
+bsattn_status carve_call_doc(const bsattn_plan* p, const bsattn_score_mod* m, void* ws, size_t ws_bytes, DocWs* w) {
+  if (!m->doc) {
+    *w = DocWs{};
+    return BSATTN_OK;
+  }
+  Carve size(nullptr);
+  carve_doc(p, size);
+  if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+  Carve c(ws);
+  *w = carve_doc(p, c);
+  return BSATTN_OK;
+}
+
+bsattn_status forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const void* q, const void* k, const float* qs,
+                          const float* ks, const void* v, const int32_t* idx, const int32_t* cnt, void* o, float* lse,
+                          void* ws, size_t ws_bytes, void* stream, AttnLayout lay) {
+  if (!p || !ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(idx) || !ok_ptr(cnt) || !ok_ptr(o) ||
+      (lse && !aligned16(lse)))
+    return BSATTN_ERR_INVALID_ARG;
+  if (p->desc.qk_fp8 && (!ok_ptr(qs) || !ok_ptr(ks))) return BSATTN_ERR_INVALID_ARG;
+  bsattn_status s = check_mod(m);
+  if (s) return s;
+  DocWs w;
+  if ((s = carve_call_doc(p, m, ws, ws_bytes, &w))) return s;
+  DeviceGuard dev(p->device);
+  if (dev.status) return dev.status;
+  if ((s = launch_doc_prep(p, m, w, (cudaStream_t)stream))) return s;
+  const ModParams d = device_mod(p, m, w);
+  return launch_attention(p, q, k, qs, ks, (const __nv_bfloat16*)v, idx, cnt, (__nv_bfloat16*)o, lse, nullptr, 0,
+                          (cudaStream_t)stream, lay, &d);
+}
+
+}  // namespace
+
+extern "C" {
+
+bsattn_status attn_mod_info(const bsattn_plan* p, bsattn_mod_info* o) {
+  if (!p || !o) return BSATTN_ERR_INVALID_ARG;
+  Carve a(nullptr), b(nullptr), c(nullptr);
+  carve_doc(p, a);
+  carve_backward_mod(p, b);
+  carve_layer_mod(p, c);
+  o->scores_workspace_bytes = o->forward_workspace_bytes = a.off;
+  o->backward_workspace_bytes = b.off;
+  o->layer_workspace_bytes = c.off;
+  return BSATTN_OK;
+}
+
+bsattn_status attn_mod_scores(const bsattn_plan* p, const bsattn_score_mod* m, const float* S, float* out, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!p || !ok_ptr(S) || !ok_ptr(out)) return BSATTN_ERR_INVALID_ARG;
+  bsattn_status s = check_mod(m);
+  if (s) return s;
+  if (p->N > 2048) return BSATTN_ERR_UNSUPPORTED;
+  DocWs w;
+  if ((s = carve_call_doc(p, m, ws, ws_bytes, &w))) return s;
+  DeviceGuard dev(p->device);
+  if (dev.status) return dev.status;
+  if ((s = launch_doc_prep(p, m, w, (cudaStream_t)stream))) return s;
+  return launch_mod_scores(p, device_mod(p, m, w), m->doc ? w.tiles : nullptr, S, out, (cudaStream_t)stream);
+}
+
+bsattn_status attn_forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const void* q, const void* k,
+                               const float* qs, const float* ks, const void* v, const int32_t* idx, const int32_t* cnt,
+                               void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  return forward_mod(p, m, q, k, qs, ks, v, idx, cnt, o, lse, ws, ws_bytes, stream, AttnLayout::Tiled);
+}
+
+bsattn_status attn_forward_natural_mod(const bsattn_plan* p, const bsattn_score_mod* m, const void* q, const void* k,
+                                       const float* qs, const float* ks, const void* v_nat, const int32_t* idx,
+                                       const int32_t* cnt, void* o_nat, float* lse_nat, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  return forward_mod(p, m, q, k, qs, ks, v_nat, idx, cnt, o_nat, lse_nat, ws, ws_bytes, stream, AttnLayout::Natural);
+}
+
+bsattn_status attn_backward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const void* q, const void* k,
+                                const void* v, const void* o, const void* d_o, const float* lse, const int32_t* idx,
+                                const int32_t* cnt, void* dq, void* dk, void* dv, float* d_slopes, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!p || !ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(o) || !ok_ptr(d_o) || !ok_ptr(lse) || !ok_ptr(idx) ||
+      !ok_ptr(cnt) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !aligned16(d_slopes))
+    return BSATTN_ERR_INVALID_ARG;
+  bsattn_status s = check_mod(m);
+  if (s) return s;
+  if (d_slopes && !m->slopes) return BSATTN_ERR_INVALID_ARG;
+  if (p->desc.qk_fp8) return BSATTN_ERR_UNSUPPORTED;
+  Carve size(nullptr);
+  carve_backward_mod(p, size);
+  if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+  DeviceGuard dev(p->device);
+  if (dev.status) return dev.status;
+  cudaStream_t st = (cudaStream_t)stream;
+  Carve c(ws);
+  const BwdModWs w = carve_backward_mod(p, c);
+  if ((s = launch_doc_prep(p, m, w.doc, st))) return s;
+  const ModParams d = device_mod(p, m, w.doc);
+  if ((s = launch_backward(p, q, k, v, o, d_o, lse, idx, cnt, dq, dk, dv, w.b, st, &d,
+                           d_slopes ? w.slope_parts : nullptr)))
+    return s;
+  if (!d_slopes) return BSATTN_OK;
+  slope_sum_kernel<<<p->desc.heads, 256, 0, st>>>(w.slope_parts, p->desc.B, p->desc.heads, attention_items(p), d_slopes);
+  return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, const bsattn_score_mod* m,
+                             const void* q_nat, const void* k_nat, const void* v_nat, void* o_nat, float* lse_nat,
+                             int32_t* idx_out, int32_t* cnt_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!p || !ok_ptr(q_nat) || !ok_ptr(k_nat) || !ok_ptr(v_nat) || !ok_ptr(o_nat) || !aligned16(lse_nat) ||
+      !aligned16(idx_out) || !aligned16(cnt_out) || ((idx_out == nullptr) != (cnt_out == nullptr)))
+    return BSATTN_ERR_INVALID_ARG;
+  bsattn_status s = BSATTN_OK;
+  if (rope && (s = check_rope(p, rope))) return s;
+  if (m && (s = check_mod(m))) return s;
+  Carve size(nullptr);
+  carve_layer_mod(p, size);
+  if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+  DeviceGuard dev(p->device);
+  if (dev.status) return dev.status;
+  cudaStream_t st = (cudaStream_t)stream;
+  Carve c(ws);
+  const LayerModWs w = carve_layer_mod(p, c);
+  const Geom g = make_geom(p);
+  int32_t* idx = idx_out ? idx_out : w.idx;
+  int32_t* cnt = cnt_out ? cnt_out : w.cnt;
+  const bool route = p->rule.kind != BSATTN_RULE_WINDOW;
+  const int32_t* doc = m ? m->doc : nullptr;
+  const void *q = q_nat, *k = k_nat;
+  if (m && (s = launch_doc_prep(p, m, w.doc, st))) return s;
+  // Rotated copies with their tile means; documents need them too where tile
+  // means or tile scales are taken, because hidden tokens must not enter those.
+  if (rope || (doc && (route || p->desc.qk_fp8))) {
+    if ((s = launch_rope(p, rope, (const __nv_bfloat16*)q_nat, w.q, (const __nv_bfloat16*)k_nat, w.k,
+                         route ? w.pq : nullptr, route ? w.pk : nullptr, false, doc, st)))
+      return s;
+    q = w.q;
+    k = w.k;
+  } else if (route) {
+    if ((s = launch_pool(g, (const __nv_bfloat16*)q, w.pq, (const __nv_bfloat16*)k, w.pk, st))) return s;
+  }
+  const ModParams d = m ? device_mod(p, m, w.doc) : ModParams{};
+  if (route) {
+    if ((s = launch_block_scores(g, w.pq, w.pk, p->scale, w.S, p->d_err, st))) return s;
+    if (m && (s = launch_mod_scores(p, d, doc ? w.doc.tiles : nullptr, w.S, w.S, st))) return s;
+  }
+  if ((s = attn_select_from_scores(p, w.S, idx, cnt, stream))) return s;
+  const void *qa = q, *ka = k;
+  if (p->desc.qk_fp8) {
+    if ((s = launch_reorder_quant(g, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, w.qc, w.kc, w.qs, w.ks, st)))
+      return s;
+    qa = w.qc;
+    ka = w.kc;
+  }
+  return launch_attention(p, qa, ka, w.qs, w.ks, (const __nv_bfloat16*)v_nat, idx, cnt, (__nv_bfloat16*)o_nat, lse_nat,
+                          nullptr, 0, st, AttnLayout::Natural, m ? &d : nullptr);
+}
+
+}  // extern "C"

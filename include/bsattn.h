@@ -335,6 +335,143 @@ bsattn_status attn_schedule_layer(const bsattn_schedule* schedule, int step, con
                                   float* lse_nat, int32_t* idx_out, int32_t* cnt_out, void* ws,
                                   size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ rotary
+ * positions and score rules. The pages have no counterpart: these are the
+ * operators that stand around the attention in the models that run it.
+ *
+ * Rotary positions. The head's first 2R features form R = (dim_t + dim_h +
+ * dim_w) / 2 pairs: pair p is features (2p, 2p + 1) in the interleaved layout
+ * and (p, p + R) in the half layout; features from 2R on pass unchanged. The
+ * first dim_t / 2 pairs turn with the token's position along t, the next
+ * dim_h / 2 along h, the last dim_w / 2 along w. Pair i of an axis with d
+ * features turns by pos * f_i, f_i = base^(-2i/d), and
+ *   (x, y) -> amplitude * (x cos - y sin, x sin + y cos).
+ * Scaling for grids longer than those trained on (factor s of the axis):
+ *   LINEAR    f_i / s
+ *   NTK       base * s^(d/(d-2)) in place of base (d > 2)
+ *   BY_PARTS  f_i (g + (1 - g) / s), g = clamp((r_i - slow) / (fast - slow),
+ *             0, 1), r_i = original * f_i / (2 pi): pairs that turn more than
+ *             `fast` times over the original extent keep their frequency,
+ *             those that turn fewer than `slow` times are interpolated.
+ * Angles are formed in fp64 (exact for every int32 position up to its last
+ * bits) and reduced before sine and cosine are taken in fp32; the rotation is
+ * fp32, rounded to bf16 once. */
+typedef enum { BSATTN_ROPE_INTERLEAVED = 0, BSATTN_ROPE_HALF = 1 } bsattn_rope_layout;
+typedef enum {
+  BSATTN_ROPE_SCALE_NONE = 0,
+  BSATTN_ROPE_SCALE_LINEAR = 1,
+  BSATTN_ROPE_SCALE_NTK = 2,
+  BSATTN_ROPE_SCALE_BY_PARTS = 3
+} bsattn_rope_scaling;
+
+typedef struct {
+  int layout;          /* bsattn_rope_layout                                  */
+  int dim[3];          /* features turned along t, h, w: even, >= 0, sum in
+                          [2, head_dim]                                       */
+  int scaling;         /* bsattn_rope_scaling                                 */
+  double base;         /* > 1, finite                                         */
+  double factor[3];    /* s of each axis: > 0, finite (unused: NONE)          */
+  double original[3];  /* BY_PARTS: original extent of each axis, > 0         */
+  double slow, fast;   /* BY_PARTS: 0 <= slow < fast                          */
+  double amplitude;    /* finite; 0 selects 1                                 */
+  int offset[3];       /* added to the token's grid coordinates (pos NULL)    */
+  const int32_t* pos;  /* NULL, or device [B, L, 3] positions (t, h, w) of
+                          every token in place of grid coordinates            */
+} bsattn_rope;
+
+/* Rotates one or two natural bf16 tensors (Q and K; x1/y1 may both be NULL),
+ * y may be the same buffer as x (other overlaps are not allowed). transpose =
+ * 1 applies the transposed rotation, i.e. takes the gradient of y to the
+ * gradient of x. pooled0/pooled1, if non-NULL, get the fp32 tile means of the
+ * rotated values over real tokens, [B, Hh, N, D], as attn_pool gives them for
+ * unrotated ones (taken before the rounding to bf16). INVALID_ARG: a field
+ * outside its range, pointers as everywhere, pooled1 without x1. */
+bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const void* x0, void* y0,
+                        const void* x1, void* y1, float* pooled0, float* pooled1, int transpose,
+                        void* stream);
+
+/* Score rules of the attention. With z = softmax_scale * q . k (times the
+ * tile scales on the e4m3 path) of a query token at (t, h, w) and a key token
+ * at (t', h', w'):
+ *   softcap > 0:  z <- softcap * tanh(z / softcap)
+ *   slopes:       z <- z - slopes[head] * (dist_t |t - t'| + dist_h |h - h'| + dist_w |w - w'|)
+ *   causal:       hidden unless t' <= t or t' < prefix[batch] (prefix NULL: 0)
+ *   doc:          hidden unless doc[query] = doc[key] and that id is >= 0
+ * in this order. Hidden pairs have probability 0; a query row that sees no
+ * key gets O = 0 and lse = -inf, and no gradient reaches or leaves it. A
+ * token with a negative id is hidden altogether: what its Q, K, V and dO
+ * rows hold, NaN and infinities included, does not reach any other row.
+ * Values at pairs that only `causal` or two different ids hide must be
+ * finite. A sequence is a grid of one column (T = length, H = W = 1, tiles
+ * of (64, 1, 1)). */
+typedef struct {
+  float softcap;                 /* 0: off; else > 0, finite                  */
+  float dist_t, dist_h, dist_w;  /* >= 0, finite                              */
+  const float* slopes;           /* NULL: off; device fp32 [heads], finite    */
+  int causal;                    /* 0 or 1                                    */
+  const int32_t* prefix;         /* NULL or device [B], frames (causal only)  */
+  const int32_t* doc;            /* NULL: off; device [B, L] natural          */
+} bsattn_score_mod;
+
+typedef struct {
+  size_t scores_workspace_bytes;    /* attn_mod_scores                        */
+  size_t forward_workspace_bytes;   /* attn_forward_mod, attn_forward_natural_mod */
+  size_t backward_workspace_bytes;  /* attn_backward_mod                      */
+  size_t layer_workspace_bytes;     /* attn_layer_mod                         */
+} bsattn_mod_info;
+bsattn_status attn_mod_info(const bsattn_plan* plan, bsattn_mod_info* out);
+
+/* The rules on block scores, between attn_block_scores and
+ * attn_select_from_scores: cap and distance bias (between the tiles' mean
+ * real token coordinates) as above, and the lowest finite fp32 number where
+ * the rules hide the whole tile pair, so that a selection ranks such pairs
+ * last (lists may still hold some; the attention skips them). Pairs hidden as
+ * a whole are those with no frame of the key tile visible to a frame of the
+ * query tile, and those whose ranges [least, greatest] of ids >= 0 do not
+ * meet (exact for ids that do not decrease along the tokens, never too much).
+ * `out` may be `scores`. UNSUPPORTED: N above 2048. `ws`:
+ * scores_workspace_bytes; may be NULL without doc. */
+bsattn_status attn_mod_scores(const bsattn_plan* plan, const bsattn_score_mod* mod, const float* scores,
+                              float* out, void* ws, size_t ws_bytes, void* stream);
+
+/* attn_forward and attn_forward_natural under score rules (any plan; cap,
+ * bias and masks are applied in fp32 inside the kernel, and key chunks that
+ * the rules hide from a whole query block are not visited). Padded rows of
+ * the tiled layout get O = 0, lse = -inf. `ws`: forward_workspace_bytes; may
+ * be NULL without doc. */
+bsattn_status attn_forward_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
+                               const void* k, const float* q_scale, const float* k_scale, const void* v,
+                               const int32_t* idx, const int32_t* cnt, void* o_tiled, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
+bsattn_status attn_forward_natural_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
+                                       const void* k, const float* q_scale, const float* k_scale,
+                                       const void* v_nat, const int32_t* idx, const int32_t* cnt, void* o_nat,
+                                       float* lse_nat, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of attn_forward_mod (same rules, o and lse from it), as
+ * attn_backward: dZ = P * (dO V^T - rowsum(dO * O)), the capped scores'
+ * derivative 1 - tanh^2 on top for dQ and dK; d_slopes, if non-NULL (fp32
+ * [heads], needs mod->slopes), gets -sum dZ * distance over the batch, summed
+ * in a fixed order. Gradients of hidden tokens and padded rows are zero.
+ * UNSUPPORTED for qk_fp8 plans. `ws`: backward_workspace_bytes. */
+bsattn_status attn_backward_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
+                                const void* k, const void* v, const void* o, const void* d_o,
+                                const float* lse, const int32_t* idx, const int32_t* cnt, void* dq, void* dk,
+                                void* dv, float* d_slopes, void* ws, size_t ws_bytes, void* stream);
+
+/* attn_layer with rotary positions on Q and K (rope, may be NULL) and score
+ * rules (mod, may be NULL): rotate into the workspace (with the tile means),
+ * block scores, rules on them, selection, attention under the rules. Results
+ * equal the step-by-step path (attn_rope with means, attn_block_scores,
+ * attn_mod_scores, attn_select_from_scores, attn_quantize_e4m3 on an e4m3
+ * plan, attn_forward_natural_mod), except that tokens with a negative id enter
+ * no tile mean (a tile of such tokens has mean 0) and no e4m3 tile scale.
+ * `ws`: attn_mod_info's layer_workspace_bytes. */
+bsattn_status attn_layer_mod(const bsattn_plan* plan, const bsattn_rope* rope, const bsattn_score_mod* mod,
+                             const void* q_nat, const void* k_nat, const void* v_nat, void* o_nat,
+                             float* lse_nat, int32_t* idx_out, int32_t* cnt_out, void* ws, size_t ws_bytes,
+                             void* stream);
+
 /* Testing hooks. Neither is part of the method (the pages have no
  * counterpart); they let tests reach the failure paths without faulting a GPU.
  *

@@ -115,3 +115,19 @@ def test_null_schedule_calls_are_invalid():
     assert lib.attn_schedule_layer(None, 0, None, None, None, None, None, None, None, None, 0,
                                    None) == 1
     lib.attn_schedule_destroy(None)  # no-op
+
+
+def test_null_rope_and_rule_calls_are_invalid():
+    from block_sparse_attention_reorder_b200 import bsattn
+    lib = bsattn._lib
+    rope, mod = bsattn.Rope(dims=(4, 2, 2)), bsattn.ScoreMod(softcap=1.0)
+    r, m = ctypes.byref(rope.raw), ctypes.byref(mod.raw)
+    assert lib.attn_rope(None, r, None, None, None, None, None, None, 0, None) == 1
+    assert lib.attn_mod_info(None, None) == 1
+    assert lib.attn_mod_scores(None, m, None, None, None, 0, None) == 1
+    assert lib.attn_forward_mod(None, m, None, None, None, None, None, None, None, None, None, None, 0, None) == 1
+    assert lib.attn_forward_natural_mod(None, m, None, None, None, None, None, None, None, None, None, None, 0,
+                                        None) == 1
+    assert lib.attn_backward_mod(None, m, None, None, None, None, None, None, None, None, None, None, None, None, None,
+                                 0, None) == 1
+    assert lib.attn_layer_mod(None, r, m, None, None, None, None, None, None, None, None, 0, None) == 1
