@@ -127,7 +127,7 @@ struct Cfg {
   static constexpr int OFF_SCAN = OFF_COL + 256;        // block-scan scratch
   static constexpr int OFF_TOK = OFF_SCAN + 64;         // epilogue: natural token of each block row
   static constexpr int OFF_TAB = OFF_TOK + 512;         // score rules: a chunk's row offsets
-  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(mod::ColTab) : 0);  // bitmaps, union list
+  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(mod::Table) : 0);  // bitmaps, union list
   static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
   static constexpr int O_PITCH = D * 2 + 16;            // epilogue staging row pitch
   static_assert(OFF_Q % 1024 == 0 && OFF_K % 1024 == 0 && OFF_V % 1024 == 0, "alignment");
@@ -180,7 +180,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   volatile int* never = reinterpret_cast<volatile int*>(misc + 3);  // stays 0: waits that ignore abort
   uint32_t* colc = reinterpret_cast<uint32_t*>(smem + C::OFF_COL);
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
-  mod::ColTab* coltab = reinterpret_cast<mod::ColTab*>(smem + C::OFF_TAB);  // score rules only
+  mod::Table* coltab = reinterpret_cast<mod::Table*>(smem + C::OFF_TAB);  // score rules only
   uint32_t* bmA = reinterpret_cast<uint32_t*>(smem + C::OFF_DYN);
   uint32_t* bmB = bmA + P.bm_words;
   uint32_t* ulist = bmB + P.bm_words;
@@ -305,7 +305,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   if (tid < 64) colc[tid] = chunk_row_code(g, tid);  // in-chunk (t, h, w) offsets of each chunk row
   int prefix = 0;
   if constexpr (MOD) {
-    if (tid < 64) mod::fill_coltab(g, coltab, tid);
     if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
   }
   if (g.cr < 64) {
@@ -412,6 +411,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     if (tid == 0) misc[2] = (uint32_t)min(tot, P.umax);
   }
   if constexpr (MOD) {
+    mod::fill_table<kThreads>(g, coltab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
     const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext,
@@ -638,19 +638,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
             const float per = -slope / unit;
             const float nw[3] = {per * M.dist[0], per * M.dist[1], per * M.dist[2]};
-            mod::add_distance<64>(reinterpret_cast<float*>(sr), coltab, 0, at, nw);
+            mod::add_distance<64>(g, reinterpret_cast<float*>(sr), coltab, 0, at, nw);
           }
           if (ext & (mod::kEdge | mod::kCausal | mod::kDoc)) {
             int vt = g.T - f.t;
             if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
-            const int32_t* docs = nullptr;
-            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
+            unsigned long long vis = mod::visible_box(g, coltab, 0, vt, g.H - f.h, g.W - f.w);
+            if (ext & mod::kDoc)
+              vis &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * nchunk + ((e >> 21) & 0x1FFu), row.id);
+            if (__any_sync(0xffffffffu, vis != ~0ull)) {
+              const uint32_t v2[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
-            for (int hq = 0; hq < 64; hq += 32) {
-              const uint32_t vis = mod::visible32(colc, hq, 0, vt, g.H - f.h, g.W - f.w, docs, row.id);
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (!((vis >> q) & 1u)) sr[hq + q] = 0xff800000u;  // -inf
+              for (int q = 0; q < 64; ++q)
+                if (!((v2[q / 32] >> (q % 32)) & 1u)) sr[q] = 0xff800000u;  // -inf
             }
           }
         } else if (edge) {  // padded keys of an edge chunk

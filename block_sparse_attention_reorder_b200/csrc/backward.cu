@@ -108,9 +108,12 @@ bsattn_status run_backward(const bsattn_plan* p, const __nv_bfloat16* q, const _
   bwd_bitmap_kernel<<<(unsigned)rows, 64, 0, st>>>(idx, cnt, g.N, p->kmax, words, w.bm, p->d_err);
   bwd_compact_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(w.bm, g.N, words, rows, w.idxT, w.cntT);
   if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
-  bsattn_status s = launch_backward_dkdv_tc(p, q, k, v, d_o, lse, w.delta, w.idxT, w.cntT, dk, dv, st, mod);
-  if (s) return s;
-  return launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st, mod, slope_parts);
+  // With score rules dQ comes first: it corrects Delta for dK.
+  bsattn_status s = BSATTN_OK;
+  if (mod && (s = launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st, mod, slope_parts))) return s;
+  s = launch_backward_dkdv_tc(p, q, k, v, d_o, lse, w.delta, w.idxT, w.cntT, dk, dv, st, mod);
+  if (s || mod) return s;
+  return launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st);
 }
 
 }  // namespace

@@ -31,6 +31,14 @@
 // the device error word, raises an abort flag, lets issued copies land,
 // drains its MMAs and frees TMEM.
 //
+// Under score rules dQ is computed first and corrects Delta on the way: the
+// rounding of O to bf16 puts an error eps_i into Delta_i, which costs dQ and
+// dK more than all other roundings where the softmax is sharp. In a row of
+// probabilities eps_i = sum_j P_ij (dP_ij - Delta_i), so the kernel sums that
+// next to a second accumulator G_i = sum_j P_ij (1 - tanh^2) K_j (one more
+// product a step) and writes dQ_i = scale (dQ_i - eps_i G_i) and Delta_i +
+// eps_i, which dK then reads.
+//
 // Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased
 // and masked scores; the step lists are filtered as in the forward. Hidden
 // pairs take no part through selects (their scores may be NaN), and the rows
@@ -48,15 +56,14 @@ namespace {
 
 constexpr int kThreads = 320;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kStages = 3;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256;
+constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColG = 384;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
 
 // Score rules: a chunk's row offsets, and every chunk's in-tile origin
 // (packed 10 bits per axis), so that a step needs no division.
 struct ModTab {
-  mod::ColTab col;
+  mod::Table col;
   uint32_t origin[kMaxChunks];
   __device__ __forceinline__ ChunkOrigin at(int c) const {
     const uint32_t v = origin[c];
@@ -64,8 +71,8 @@ struct ModTab {
   }
 };
 template <int NT>
-__device__ __forceinline__ void fill_modtab(const Geom& g, ModTab* tab) {
-  if (threadIdx.x < 64) mod::fill_coltab(g, &tab->col, threadIdx.x);
+__device__ __forceinline__ void fill_modtab(const Geom& g, ModTab* tab, const uint32_t* colc) {
+  mod::fill_table<NT>(g, &tab->col, colc);
   for (int c = threadIdx.x; c < g.nchunk; c += NT) {
     const ChunkOrigin o = chunk_origin(g, c);
     tab->origin[c] = (uint32_t)o.dt | ((uint32_t)o.dh << 10) | ((uint32_t)o.dw << 20);
@@ -91,10 +98,11 @@ struct DqParams {
 
 struct DqParamsMod : DqParams {
   ModParams mod;
+  float* delta_out;    // delta, corrected
   float* slope_parts;  // null, or [B * heads, CTAs per head]: the slope gradient's parts
 };
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 struct DqCfg {
   static constexpr int QRB = D * 2;                  // row bytes
   static constexpr int QBLK = QRB / 128;             // 128-byte column blocks
@@ -218,12 +226,12 @@ __device__ __forceinline__ void compact_steps(const Geom& g, const uint32_t* bmA
   if (tid == 0) *count = (uint32_t)min(tot, cap);
 }
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ std::conditional_t<MOD, DqParamsMod, DqParams> P) {
-  using C = DqCfg<D, MOD>;
+  using C = DqCfg<D, MOD, kStages>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -278,7 +286,6 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   ModTab* tab = reinterpret_cast<ModTab*>(smem + C::OFF_TAB);  // score rules only
   int prefix = 0;
   if constexpr (MOD) {
-    fill_modtab<kThreads>(g, tab);
     if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
   }
   for (int w = tid; w < 2 * P.bm_words; w += kThreads) bmA[w] = 0u;
@@ -319,6 +326,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   __syncthreads();
   compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
   if constexpr (MOD) {
+    fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
     const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, nullptr, steps, scan);
@@ -410,8 +418,9 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // 16 keys per MMA: 2048 bytes of the K tile
           const uint64_t dk = tc::smem_desc(sb + C::OFF_K + s * C::T_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
-          tc::mma_ts_f16(tmem + kColDQ, dsA + (kk < 2 ? kk * 8 : 32 + (kk - 2) * 8), dk, idQ,
-                         (n > 0 || kk > 0) ? 1u : 0u);
+          const uint32_t acol = kk < 2 ? kk * 8 : 32 + (kk - 2) * 8, acc = (n > 0 || kk > 0) ? 1u : 0u;
+          tc::mma_ts_f16(tmem + kColDQ, dsA + acol, dk, idQ, acc);
+          if (MOD) tc::mma_ts_f16(tmem + kColG, dsA + kColDP + acol, dk, idQ, acc);
         }
         tc::mma_commit(bar_empty(s));
         if (n + 2 < L && !issue_sdp(n + 2)) {
@@ -456,6 +465,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint32_t sbuf = tmem + lane_base + kColS + (n & 1) * 64 + 32 * part;
       const uint32_t pbuf = tmem + lane_base + kColDP + (n & 1) * 64 + 32 * part;
       uint32_t dsw[16];
+      uint32_t gw[MOD ? 16 : 1];  // P (1 - tanh^2)
       if constexpr (MOD) {
         if ((uext[n] & mod::kHidden) && tid < 64) {  // K rows of hidden tokens (S has been formed)
           const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
@@ -474,9 +484,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
             int vt = g.T - f.t;
             if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
-            const int32_t* docs = nullptr;
-            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
-            vis = mod::visible32(colc, 32 * part, 0, vt, g.H - f.h, g.W - f.w, docs, row.id);
+            unsigned long long all = mod::visible_box(g, &tab->col, 0, vt, g.H - f.h, g.W - f.w);
+            if (ext & mod::kDoc)
+              all &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.nchunk + ((e >> 21) & 0x1FFu), row.id);
+            vis = (uint32_t)(all >> (32 * part));
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32_wait(sbuf, sr);
@@ -493,29 +504,38 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int q = 0; q < 32; ++q) far[q] = 0.f;
           if (M.slopes) {
             const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
-            mod::add_distance<32>(far, &tab->col, 32 * part, at, M.dist);
+            mod::add_distance<32>(g, far, &tab->col, 32 * part, at, M.dist);
           }
           const float s2 = -slope * mod::kLog2e;
+          auto form = [&](auto masked) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float d2[2];
+            for (int q = 0; q < 16; ++q) {
+              float d2[2], g2[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int x = 2 * q + u;
-              const float th = __uint_as_float(sr[x]);
-              const bool see = (vis >> x) & 1u;
-              const float p = see ? tc::ex2(fmaf(far[x], s2, fmaf(th, c2, -lse2))) : 0.f;
-              const float w = see ? p * (__uint_as_float(pr[x]) - dlt) : 0.f;
-              if (P.slope_parts) {
+              for (int u = 0; u < 2; ++u) {
+                const int x = 2 * q + u;
+                const float th = __uint_as_float(sr[x]);
+                float p = tc::ex2(fmaf(far[x], s2, fmaf(th, c2, -lse2)));
+                float w = p * (__uint_as_float(pr[x]) - dlt);
+                if (masked && !((vis >> x) & 1u)) p = w = 0.f;
                 sw += w;
-                swd = fmaf(w, far[x], swd);
-                spd = fmaf(p, far[x], spd);
+                if (P.slope_parts) {
+                  swd = fmaf(w, far[x], swd);
+                  spd = fmaf(p, far[x], spd);
+                }
+                const float gain = cap ? fmaf(-th, th, 1.f) : 1.f;
+                d2[u] = masked && cap && !((vis >> x) & 1u) ? 0.f : w * gain;
+                g2[u] = masked && cap && !((vis >> x) & 1u) ? 0.f : p * gain;
               }
-              d2[u] = cap ? (see ? w * fmaf(-th, th, 1.f) : 0.f) : w;
+              __nv_bfloat162 hv = __floats2bfloat162_rn(d2[0], d2[1]), hg = __floats2bfloat162_rn(g2[0], g2[1]);
+              dsw[q] = *reinterpret_cast<uint32_t*>(&hv);
+              gw[q] = *reinterpret_cast<uint32_t*>(&hg);
             }
-            __nv_bfloat162 hv = __floats2bfloat162_rn(d2[0], d2[1]);
-            dsw[q] = *reinterpret_cast<uint32_t*>(&hv);
-          }
+          };
+          if (__all_sync(0xffffffffu, vis == 0xffffffffu))
+            form(std::false_type{});
+          else
+            form(std::true_type{});
         }
       } else if (!MOD && keep) {
         const uint32_t ext = uext[n];
@@ -543,7 +563,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q) dsw[q] = 0u;
+        if constexpr (MOD) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) gw[q] = 0u;
+        }
       }
+      if constexpr (MOD) tc::tmem_st16(pbuf, gw);
       tc::tmem_st16(sbuf, dsw);  // dS of this half over the first 16 columns of its S
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -562,23 +587,29 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       tc::fence_after_sync();
     }
+    float eps = 0.f;
     if constexpr (MOD) {
+      // The two halves' sums. With w = P (dP - Delta) for any Delta and sum P
+      // = 1: eps = sum w, and the row's share of -sum dZ dist is eps (sum P
+      // dist) - sum w dist.
+      float* red = reinterpret_cast<float*>(smem + C::OFF_V);  // the V ring is no longer read
+      const bool use = ok && L > 0;
+      if (use) {
+        red[3 * tid] = sw;
+        red[3 * tid + 1] = swd;
+        red[3 * tid + 2] = spd;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+      float v = 0.f;
+      if (use && row.live) {
+        const int o = 3 * (tid ^ 128);
+        eps = sw + red[o];
+        if (part == 0) {
+          P.delta_out[lrow] = dlt + eps;
+          v = eps * (spd + red[o + 2]) - (swd + red[o + 1]);
+        }
+      }
       if (P.slope_parts) {
-        // Row r's share of -sum dZ dist. With w = P (dP - Delta) for any Delta
-        // and sum P = 1, dZ = w - P sum w: the rounding of O in Delta drops out.
-        float* red = reinterpret_cast<float*>(smem + C::OFF_V);  // the V ring is no longer read
-        const bool use = ok && L > 0;
-        if (use) {
-          red[3 * tid] = sw;
-          red[3 * tid + 1] = swd;
-          red[3 * tid + 2] = spd;
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-        float v = 0.f;
-        if (use && part == 0 && row.live) {
-          const int o = 3 * (tid + 128);
-          v = (sw + red[o]) * (spd + red[o + 2]) - (swd + red[o + 1]);
-        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (part == 0 && lane == 0) scan[warp] = __float_as_int(v);
@@ -600,6 +631,13 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int q = 0; q < 32; ++q) o[q] = 0u;
       }
       if constexpr (MOD) {
+        if (ok && L > 0) {
+          uint32_t gr[32];
+          tc::tmem_ld32_wait(tmem + lane_base + kColG + col, gr);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            o[q] = __float_as_uint(fmaf(-eps, __uint_as_float(gr[q]), __uint_as_float(o[q])));
+        }
         if (!row.live) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = 0u;
@@ -636,10 +674,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* d_o,
                      const std::conditional_t<MOD, DqParamsMod, DqParams>& prm, cudaStream_t st) {
-  using C = DqCfg<D, MOD>;
+  using C = DqCfg<D, MOD, kStages>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mdo, mk, mv;
@@ -651,7 +689,7 @@ bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const v
     return BSATTN_ERR_CUDA;
   const size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = bwd_dq_tc_kernel<D, MOD>;
+  auto kern = bwd_dq_tc_kernel<D, MOD, kStages>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -693,7 +731,7 @@ struct KvParamsMod : KvParams {
   ModParams mod;
 };
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 struct KvCfg {
   static constexpr int QRB = D * 2;
   static constexpr int QBLK = QRB / 128;
@@ -717,12 +755,12 @@ struct KvCfg {
   static_assert(2 * 128 * O_PITCH <= OFF_BAR - OFF_RING, "epilogue staging fits in the ring");
 };
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ std::conditional_t<MOD, KvParamsMod, KvParams> P) {
-  using C = KvCfg<D, MOD>;
+  using C = KvCfg<D, MOD, kStages>;
   constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 256 + D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -786,7 +824,6 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   ModTab* tab = reinterpret_cast<ModTab*>(smem + C::OFF_TAB);  // score rules only
   int prefix = 0;
   if constexpr (MOD) {
-    fill_modtab<kThreads>(g, tab);
     if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
   }
   for (int w = tid; w < 2 * P.bm_words; w += kThreads) bmA[w] = 0u;
@@ -818,6 +855,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
   if constexpr (MOD) {
+    fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
     const int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, nullptr, steps, scan);
@@ -988,9 +1026,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
             // Queries at or behind the key's frame, all of them for a key of the prefix.
             const int lo = M.causal && row.at.t >= prefix ? row.at.t - f.t : 0;
-            const int32_t* docs = nullptr;
-            if (ext & mod::kDoc) docs = M.doc_rows + ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
-            vis = mod::visible32(colc, 32 * part, lo, g.T - f.t, g.H - f.h, g.W - f.w, docs, row.id);
+            unsigned long long all = mod::visible_box(g, &tab->col, lo, g.T - f.t, g.H - f.h, g.W - f.w);
+            if (ext & mod::kDoc)
+              all &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.nchunk + ((e >> 21) & 0x1FFu), row.id);
+            vis = (uint32_t)(all >> (32 * part));
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32_wait(sbuf, sr);
@@ -1008,24 +1047,30 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
             const float s2 = -slope * mod::kLog2e;
             const float nw[3] = {s2 * M.dist[0], s2 * M.dist[1], s2 * M.dist[2]};
-            mod::add_distance<32>(y, &tab->col, 32 * part, at, nw);
+            mod::add_distance<32>(g, y, &tab->col, 32 * part, at, nw);
           }
+          auto form = [&](auto masked) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float pp[2], d2[2];
+            for (int q = 0; q < 16; ++q) {
+              float pp[2], d2[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int x = 2 * q + u;
-              const float th = __uint_as_float(sr[x]);
-              const bool see = (vis >> x) & 1u;
-              pp[u] = see ? tc::ex2(y[x]) : 0.f;
-              const float w = pp[u] * (__uint_as_float(pr[x]) - ld[64 + 32 * part + x]);
-              d2[u] = see ? (cap ? w * fmaf(-th, th, 1.f) : w) : 0.f;
+              for (int u = 0; u < 2; ++u) {
+                const int x = 2 * q + u;
+                const float th = __uint_as_float(sr[x]);
+                pp[u] = tc::ex2(y[x]);
+                d2[u] = pp[u] * (__uint_as_float(pr[x]) - ld[64 + 32 * part + x]);
+                if (cap) d2[u] *= fmaf(-th, th, 1.f);
+                if (masked && !((vis >> x) & 1u)) pp[u] = d2[u] = 0.f;
+              }
+              __nv_bfloat162 hp = __floats2bfloat162_rn(pp[0], pp[1]), hd = __floats2bfloat162_rn(d2[0], d2[1]);
+              pw[q] = *reinterpret_cast<uint32_t*>(&hp);
+              dw[q] = *reinterpret_cast<uint32_t*>(&hd);
             }
-            __nv_bfloat162 hp = __floats2bfloat162_rn(pp[0], pp[1]), hd = __floats2bfloat162_rn(d2[0], d2[1]);
-            pw[q] = *reinterpret_cast<uint32_t*>(&hp);
-            dw[q] = *reinterpret_cast<uint32_t*>(&hd);
-          }
+          };
+          if (__all_sync(0xffffffffu, vis == 0xffffffffu))
+            form(std::false_type{});
+          else
+            form(std::true_type{});
         }
       } else if (!MOD && keep) {
         const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
@@ -1132,10 +1177,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   }
 }
 
-template <int D, bool MOD>
+template <int D, bool MOD, int kStages>
 bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* d_o,
                        const std::conditional_t<MOD, KvParamsMod, KvParams>& prm, cudaStream_t st) {
-  using C = KvCfg<D, MOD>;
+  using C = KvCfg<D, MOD, kStages>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mdo, mk, mv;
@@ -1147,7 +1192,7 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
     return BSATTN_ERR_CUDA;
   const size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = bwd_dkdv_tc_kernel<D, MOD>;
+  auto kern = bwd_dkdv_tc_kernel<D, MOD, kStages>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -1158,8 +1203,22 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
 
 }  // namespace
 
+// Shared memory of a launch: the configuration's fixed part, two list bitmaps
+// and two words per step.
+template <class C, class P>
+static size_t smem_of(const P& prm) {
+  return 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
+}
+// Whether a deeper ring leaves room for the step lists. Under score rules the
+// ring holds four stages at D = 128 and six at D = 64: with three the step
+// time is the latency of a stage's loads, PLACEHOLDER.
+template <class C, class P>
+static bool fits(const P& prm) {
+  return smem_of<C>(prm) <= 227 * 1024;
+}
+
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
-                                    const void* d_o, const float* lse, const float* delta, const int32_t* idx,
+                                    const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod,
                                     float* slope_parts) {
   DqParamsMod prm;
@@ -1182,10 +1241,15 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
   const bool d128 = p->desc.head_dim == 128;
   if (mod) {
     prm.mod = *mod;
+    prm.delta_out = delta;
     prm.slope_parts = slope_parts;
-    return d128 ? run_dq<128, true>(p, q, k, v, d_o, prm, st) : run_dq<64, true>(p, q, k, v, d_o, prm, st);
+    if (d128)
+      return fits<DqCfg<128, true, 4>>(prm) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)
+                                            : run_dq<128, true, 3>(p, q, k, v, d_o, prm, st);
+    return fits<DqCfg<64, true, 6>>(prm) ? run_dq<64, true, 6>(p, q, k, v, d_o, prm, st)
+                                         : run_dq<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
-  return d128 ? run_dq<128, false>(p, q, k, v, d_o, prm, st) : run_dq<64, false>(p, q, k, v, d_o, prm, st);
+  return d128 ? run_dq<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dq<64, false, 3>(p, q, k, v, d_o, prm, st);
 }
 
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
@@ -1212,7 +1276,11 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
   const bool d128 = p->desc.head_dim == 128;
   if (mod) {
     prm.mod = *mod;
-    return d128 ? run_dkdv<128, true>(p, q, k, v, d_o, prm, st) : run_dkdv<64, true>(p, q, k, v, d_o, prm, st);
+    if (d128)
+      return fits<KvCfg<128, true, 4>>(prm) ? run_dkdv<128, true, 4>(p, q, k, v, d_o, prm, st)
+                                            : run_dkdv<128, true, 3>(p, q, k, v, d_o, prm, st);
+    return fits<KvCfg<64, true, 6>>(prm) ? run_dkdv<64, true, 6>(p, q, k, v, d_o, prm, st)
+                                         : run_dkdv<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
-  return d128 ? run_dkdv<128, false>(p, q, k, v, d_o, prm, st) : run_dkdv<64, false>(p, q, k, v, d_o, prm, st);
+  return d128 ? run_dkdv<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dkdv<64, false, 3>(p, q, k, v, d_o, prm, st);
 }

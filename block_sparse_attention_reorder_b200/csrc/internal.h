@@ -152,6 +152,16 @@ bsattn_status launch_select_topp(int rows, int N, int k, double p, const float* 
 bsattn_status launch_broadcast_lists(int bh, int N, int kmax, const int32_t* src_idx,
                                      const int32_t* src_cnt, int32_t* idx, int32_t* cnt,
                                      cudaStream_t st);
+// Document ids of one 64-row chunk: the least and greatest id >= 0 and how
+// many tokens have one and have a negative one; and up to four ids, each with
+// the rows that carry it (unused: kNoId; id.w = kManyIds: there are more).
+constexpr int kNoId = -1, kManyIds = -3;
+struct alignas(16) DocChunk {
+  int4 range;
+  int4 id;
+  unsigned long long rows[4];
+};
+
 // Score rules of one call on the device (attn_*_mod). doc_rows and doc_chunks
 // live in the call's workspace.
 struct ModParams {
@@ -161,7 +171,7 @@ struct ModParams {
   int causal;
   const int32_t* prefix;     // null: 0
   const int32_t* doc_rows;   // null: no documents; [B, N, V] ids in tile order, padded slots -1
-  const int4* doc_chunks;    // [B, N, nchunk] (least, greatest id >= 0, tokens with one, tokens without)
+  const DocChunk* doc_chunks;  // [B, N, nchunk]
   int sh_h, sh_w;            // bits of a tile's h and w coordinates (packed step coordinates)
 };
 
@@ -202,9 +212,9 @@ bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k
                               const ModParams* mod = nullptr, float* slope_parts = nullptr);
 
 // dQ of the backward on the tensor cores (tiled bf16 q, k, v, dO; lse and
-// rowsum(dO * O) tiled fp32).
+// rowsum(dO * O) tiled fp32; with score rules delta is corrected in place).
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
-                                    const void* d_o, const float* lse, const float* delta, const int32_t* idx,
+                                    const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod = nullptr,
                                     float* slope_parts = nullptr);
 

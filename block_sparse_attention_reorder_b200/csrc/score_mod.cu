@@ -24,16 +24,14 @@ struct Carve {
 // Ids in tile order, and their ranges per 64-row chunk and per tile.
 struct DocWs {
   int32_t* rows;  // [B, N, V]
-  int4* chunks;   // [B, N, nchunk]
-  int2* tiles;    // [B, N] least and greatest id >= 0 (INT_MAX, -1: none)
+  DocChunk* chunks;  // [B, N, nchunk]
 };
 
 DocWs carve_doc(const bsattn_plan* p, Carve& c) {
   const size_t bn = (size_t)p->desc.B * p->N;
   DocWs w;
   w.rows = (int32_t*)c.take(bn * p->V * sizeof(int32_t));
-  w.chunks = (int4*)c.take(bn * p->nchunk * sizeof(int4));
-  w.tiles = (int2*)c.take(bn * sizeof(int2));
+  w.chunks = (DocChunk*)c.take(bn * p->nchunk * sizeof(DocChunk));
   return w;
 }
 
@@ -82,37 +80,63 @@ LayerModWs carve_layer_mod(const bsattn_plan* p, Carve& c) {
   return w;
 }
 
-// One CTA of two warps per (tile, batch): the ids of the tile's rows, and
-// their ranges. A few bytes per token; bound by its launch.
-__global__ void __launch_bounds__(64) doc_prep_kernel(Geom g, const int32_t* __restrict__ doc, DocWs w) {
-  __shared__ int4 part[2];
-  const int j = blockIdx.x, b = blockIdx.y, r = threadIdx.x;
-  const int t0 = j / (g.nH * g.nW) * g.tt, h0 = j / g.nW % g.nH * g.th, w0 = j % g.nW * g.tw;
-  const uint32_t code = chunk_row_code(g, r);
-  int2 tile = make_int2(INT_MAX, -1);
-  for (int c = 0; c < g.nchunk; ++c) {
-    const ChunkOrigin o = chunk_origin(g, c);
-    const int t = t0 + o.dt + (int)(code & 0xffu), h = h0 + o.dh + (int)((code >> 8) & 0xffu),
-              x = w0 + o.dw + (int)((code >> 16) & 0xffu);
-    const bool real = r < g.cr && t < g.T && h < g.H && x < g.W;
-    const int id = real ? doc[(size_t)b * g.L + (t * g.H + h) * g.W + x] : -1;
-    w.rows[((size_t)b * g.N + j) * g.V + 64 * c + r] = id < 0 ? -1 : id;
-    int lo = id >= 0 ? id : INT_MAX, hi = id >= 0 ? id : -1, with = id >= 0, without = real && id < 0;
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    with = __reduce_add_sync(0xffffffffu, with);
-    without = __reduce_add_sync(0xffffffffu, without);
-    if (r % 32 == 0) part[r / 32] = make_int4(lo, hi, with, without);
-    __syncthreads();
-    if (r == 0) {
-      const int4 p = part[0], q = part[1];
-      const int4 all = make_int4(min(p.x, q.x), max(p.y, q.y), p.z + q.z, p.w + q.w);
-      w.chunks[((size_t)b * g.N + j) * g.nchunk + c] = all;
-      tile = make_int2(min(tile.x, all.x), max(tile.y, all.y));
+// One warp per (64-row chunk, batch), two rows a lane: the ids in tile order,
+// their range, and up to four ids with their rows. A few bytes per token;
+// bound by its launch.
+constexpr int kPrepWarps = 4;
+__global__ void __launch_bounds__(32 * kPrepWarps) doc_prep_kernel(Geom g, const int32_t* __restrict__ doc, DocWs w) {
+  const int lane = threadIdx.x % 32, b = blockIdx.y;
+  const long long n = (long long)blockIdx.x * kPrepWarps + threadIdx.x / 32;  // chunk of the batch
+  if (n >= (long long)g.N * g.nchunk) return;
+  const int j = (int)(n / g.nchunk), c = (int)(n % g.nchunk);
+  const ChunkOrigin o = chunk_origin(g, c);
+  const int t0 = j / (g.nH * g.nW) * g.tt + o.dt, h0 = j / g.nW % g.nH * g.th + o.dh, w0 = j % g.nW * g.tw + o.dw;
+  int id[2];
+  int without = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = lane + 32 * x;
+    const uint32_t code = chunk_row_code(g, r);
+    const int t = t0 + (int)(code & 0xffu), h = h0 + (int)((code >> 8) & 0xffu), v = w0 + (int)((code >> 16) & 0xffu);
+    const bool real = r < g.cr && t < g.T && h < g.H && v < g.W;
+    id[x] = real ? doc[(size_t)b * g.L + (t * g.H + h) * g.W + v] : -1;
+    if (id[x] < 0) {
+      id[x] = -1;
+      without += real ? 1 : 0;
     }
-    __syncthreads();
+    w.rows[((size_t)b * g.N + j) * g.V + 64 * c + r] = id[x];
   }
-  if (r == 0) w.tiles[(size_t)b * g.N + j] = tile;
+  const unsigned all = 0xffffffffu;
+  DocChunk k;
+  k.range.x = __reduce_min_sync(all, min(id[0] < 0 ? INT_MAX : id[0], id[1] < 0 ? INT_MAX : id[1]));
+  k.range.y = __reduce_max_sync(all, max(id[0], id[1]));
+  k.range.z = __reduce_add_sync(all, (id[0] >= 0) + (id[1] >= 0));
+  k.range.w = __reduce_add_sync(all, without);
+  int ids[4];
+  int left[2] = {id[0], id[1]};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {  // the least id not yet taken; greatest int as an id shares the code of "none left"
+    const int next = __reduce_min_sync(all, min(left[0] < 0 ? INT_MAX : left[0], left[1] < 0 ? INT_MAX : left[1]));
+    const uint32_t lo = __ballot_sync(all, left[0] == next), hi = __ballot_sync(all, left[1] == next);
+    ids[e] = lo | hi ? next : kNoId;
+    k.rows[e] = ((unsigned long long)hi << 32) | lo;
+    if (left[0] == next) left[0] = -1;
+    if (left[1] == next) left[1] = -1;
+  }
+  if (__any_sync(all, left[0] >= 0 || left[1] >= 0)) ids[3] = kManyIds;
+  k.id = make_int4(ids[0], ids[1], ids[2], ids[3]);
+  if (lane == 0) w.chunks[((size_t)b * g.N + j) * g.nchunk + c] = k;
+}
+
+// Least and greatest id >= 0 of each tile (INT_MAX, -1: none), from its chunks.
+__device__ __forceinline__ int2 tile_ids(const Geom& g, const DocChunk* chunks, int b, int j) {
+  int2 r = make_int2(INT_MAX, -1);
+  for (int c = 0; c < g.nchunk; ++c) {
+    const int4 x = __ldg(&chunks[((size_t)b * g.N + j) * g.nchunk + c].range);
+    r.x = min(r.x, x.x);
+    r.y = max(r.y, x.y);
+  }
+  return r;
 }
 
 // The rules on block scores, S' from S. Memory bound (8 bytes an entry): a
@@ -127,18 +151,19 @@ struct TileMeta {
   int first, last;  // frames
   int2 ids;
 };
-__device__ __forceinline__ TileMeta tile_meta(const Geom& g, int j, int b, const int2* ids) {
+__device__ __forceinline__ TileMeta tile_meta(const Geom& g, int j, int b, const DocChunk* ids) {
   const int t0 = j / (g.nH * g.nW) * g.tt, h0 = j / g.nW % g.nH * g.th, w0 = j % g.nW * g.tw;
   const int vt = min(g.tt, g.T - t0), vh = min(g.th, g.H - h0), vw = min(g.tw, g.W - w0);
   TileMeta m{t0 + 0.5f * (vt - 1), h0 + 0.5f * (vh - 1), w0 + 0.5f * (vw - 1), t0, t0 + vt - 1, make_int2(0, 0)};
-  if (ids) m.ids = __ldg(ids + (size_t)b * g.N + j);
+  if (ids) m.ids = tile_ids(g, ids, b, j);
   return m;
 }
 
 template <bool VEC>
 __global__ void __launch_bounds__(kScoreThreads)
-mod_scores_kernel(Geom g, ModParams m, const int2* __restrict__ ids, const float* S, float* out) {
+mod_scores_kernel(Geom g, ModParams m, const float* S, float* out) {
   __shared__ TileMeta rowm[kScoreRows];
+  const DocChunk* ids = m.doc_chunks;
   const int N = g.N, bh = blockIdx.z, b = bh / g.Hh, head = bh % g.Hh;
   const int i0 = blockIdx.y * kScoreRows, rows = min(kScoreRows, N - i0);
   const int j0 = 4 * (blockIdx.x * kScoreThreads + threadIdx.x);
@@ -252,19 +277,20 @@ ModParams device_mod(const bsattn_plan* p, const bsattn_score_mod* m, const DocW
 bsattn_status launch_doc_prep(const bsattn_plan* p, const bsattn_score_mod* m, const DocWs& w, cudaStream_t st) {
   if (!m->doc) return BSATTN_OK;
   if (p->desc.B > 65535) return BSATTN_ERR_UNSUPPORTED;
-  doc_prep_kernel<<<dim3(p->N, p->desc.B), 64, 0, st>>>(make_geom(p), m->doc, w);
+  const long long chunks = (long long)p->N * p->nchunk;
+  doc_prep_kernel<<<dim3((unsigned)((chunks + kPrepWarps - 1) / kPrepWarps), p->desc.B), 32 * kPrepWarps, 0, st>>>(
+      make_geom(p), m->doc, w);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
-bsattn_status launch_mod_scores(const bsattn_plan* p, const ModParams& d, const int2* ids, const float* S, float* out,
-                                cudaStream_t st) {
+bsattn_status launch_mod_scores(const bsattn_plan* p, const ModParams& d, const float* S, float* out, cudaStream_t st) {
   const Geom g = make_geom(p);
   if ((long long)g.B * g.Hh > 65535) return BSATTN_ERR_UNSUPPORTED;
   dim3 grid((g.N + 4 * kScoreThreads - 1) / (4 * kScoreThreads), (g.N + kScoreRows - 1) / kScoreRows, g.B * g.Hh);
   if (g.N % 4 == 0)  // every row starts on 16 bytes
-    mod_scores_kernel<true><<<grid, kScoreThreads, 0, st>>>(g, d, ids, S, out);
+    mod_scores_kernel<true><<<grid, kScoreThreads, 0, st>>>(g, d, S, out);
   else
-    mod_scores_kernel<false><<<grid, kScoreThreads, 0, st>>>(g, d, ids, S, out);
+    mod_scores_kernel<false><<<grid, kScoreThreads, 0, st>>>(g, d, S, out);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
@@ -328,7 +354,7 @@ bsattn_status attn_mod_scores(const bsattn_plan* p, const bsattn_score_mod* m, c
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
   if ((s = launch_doc_prep(p, m, w, (cudaStream_t)stream))) return s;
-  return launch_mod_scores(p, device_mod(p, m, w), m->doc ? w.tiles : nullptr, S, out, (cudaStream_t)stream);
+  return launch_mod_scores(p, device_mod(p, m, w), S, out, (cudaStream_t)stream);
 }
 
 bsattn_status attn_forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const void* q, const void* k,
@@ -411,7 +437,7 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
   const ModParams d = m ? device_mod(p, m, w.doc) : ModParams{};
   if (route) {
     if ((s = launch_block_scores(g, w.pq, w.pk, p->scale, w.S, p->d_err, st))) return s;
-    if (m && (s = launch_mod_scores(p, d, doc ? w.doc.tiles : nullptr, w.S, w.S, st))) return s;
+    if (m && (s = launch_mod_scores(p, d, w.S, w.S, st))) return s;
   }
   if ((s = attn_select_from_scores(p, w.S, idx, cnt, stream))) return s;
   const void *qa = q, *ka = k;

@@ -13,19 +13,26 @@ namespace mod {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHiddenDoc = -2;  // a query id that equals no key's
 
-// tanh for |u| <= kSmall: u + u^3 P(u^2), P of degree 4 fitted to
-// (tanh(u) / u - 1) / u^2 for the least maximum relative error of tanh
-// (Lawson's iteratively reweighted least squares): 3.2e-8, 1.0e-7 evaluated
-// in fp32. Eight FMA-pipe operations, four on packed pairs.
-constexpr float kSmall = 0.75f;
+// tanh for small |u|: u (1 + v P(v)), v = u^2, P fitted to (tanh(u) / u - 1)
+// / v for the least maximum relative error of tanh (Lawson's iteratively
+// reweighted least squares): degree 4 on |u| <= 0.75 (3.2e-8; 1.0e-7 with
+// fp32 evaluation), degree 2 on |u| <= 0.375 (7.0e-8; 1.3e-7). Six and eight
+// FMA-pipe operations on packed pairs, the SFU stays free for the softmax.
+constexpr float kSmall = 0.75f, kTiny = 0.375f;
+__device__ __forceinline__ float2 bc(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 tanh_tiny2(float2 u) {
+  const float2 v = __fmul2_rn(u, u);
+  float2 p = __ffma2_rn(bc(-0.04848729074001312f), v, bc(0.1328972578048706f));
+  p = __ffma2_rn(p, v, bc(-0.33332332968711853f));
+  return __fmul2_rn(u, __ffma2_rn(p, v, bc(1.f)));
+}
 __device__ __forceinline__ float2 tanh_small2(float2 u) {
   const float2 v = __fmul2_rn(u, u);
-  float2 p = __ffma2_rn(make_float2(-0.004769490100443363f, -0.004769490100443363f), v,
-                        make_float2(0.019664913415908813f, 0.019664913415908813f));
-  p = __ffma2_rn(p, v, make_float2(-0.0533902570605278f, -0.0533902570605278f));
-  p = __ffma2_rn(p, v, make_float2(0.13326521217823029f, 0.13326521217823029f));
-  p = __ffma2_rn(p, v, make_float2(-0.3333306908607483f, -0.3333306908607483f));
-  return __ffma2_rn(__fmul2_rn(v, u), p, u);
+  float2 p = __ffma2_rn(bc(-0.004769490100443363f), v, bc(0.019664913415908813f));
+  p = __ffma2_rn(p, v, bc(-0.0533902570605278f));
+  p = __ffma2_rn(p, v, bc(0.13326521217823029f));
+  p = __ffma2_rn(p, v, bc(-0.3333306908607483f));
+  return __fmul2_rn(u, __ffma2_rn(p, v, bc(1.f)));
 }
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -38,18 +45,26 @@ __device__ __forceinline__ float tanh_any(float u) {
   return fmaf(-2.f, rcp(tc::ex2(u * (2.f * kLog2e)) + 1.f), 1.f);
 }
 
-// Replaces raw scores s[] by u = tanh(k s) (k = scale / cap). The polynomial
-// serves a whole warp's values when all are small, which usual scores under a
-// usual cap are; else the SFU form does, and the polynomial where |u| is
-// small, so that a value's tanh does not depend on its neighbours.
+// Replaces raw scores s[] by tanh(k s) (k = scale / cap). The polynomials
+// serve a whole warp's values when the largest is small, which usual scores
+// under a usual cap are; else the SFU form does, and the polynomial where |u|
+// is small. The forms agree to about 2e-7 of the value.
 template <int N>
 __device__ __forceinline__ void tanh_scores(uint32_t* s, float k) {
-  float mx = 0.f;
+  float mx4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int q = 0; q < N; ++q) mx = fmaxf(mx, fabsf(__uint_as_float(s[q])));
-  const bool small = mx * fabsf(k) <= kSmall;
-  const float2 k2 = make_float2(k, k);
-  if (__all_sync(0xffffffffu, small)) {
+  for (int q = 0; q < N; q += 2)
+    mx4[(q / 2) & 3] = tc::fmax3(mx4[(q / 2) & 3], fabsf(__uint_as_float(s[q])), fabsf(__uint_as_float(s[q + 1])));
+  const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fabsf(k);
+  const float2 k2 = bc(k);
+  if (__all_sync(0xffffffffu, mx <= kTiny)) {
+#pragma unroll
+    for (int q = 0; q < N; q += 2) {
+      const float2 t = tanh_tiny2(__fmul2_rn(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), k2));
+      s[q] = __float_as_uint(t.x);
+      s[q + 1] = __float_as_uint(t.y);
+    }
+  } else if (__all_sync(0xffffffffu, mx <= kSmall)) {
 #pragma unroll
     for (int q = 0; q < N; q += 2) {
       const float2 t = tanh_small2(__fmul2_rn(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), k2));
@@ -98,7 +113,7 @@ __device__ __forceinline__ Half half_of(const Geom& g, const ModParams& m, int b
   const ChunkOrigin o = chunk_origin(g, chunk);
   const int t0 = tile / (g.nH * g.nW) * g.tt + o.dt;
   Half r{t0, min(t0 + g.ct - 1, g.T - 1), make_int4(0, 0, 1, 0)};
-  if (m.doc_chunks) r.ids = __ldg(m.doc_chunks + ((size_t)b * g.N + tile) * g.nchunk + chunk);
+  if (m.doc_chunks) r.ids = __ldg(&m.doc_chunks[((size_t)b * g.N + tile) * g.nchunk + chunk].range);
   return r;
 }
 
@@ -186,27 +201,104 @@ __device__ __forceinline__ Row row_of(const Geom& g, const ModParams& m, int b, 
   return x;
 }
 
-// Shared tables of a chunk's 64 rows: offsets from its first token along each
-// axis, as fp32.
-struct ColTab {
-  float d[3][64];
+// Shared tables of a chunk's 64 rows (columns of a step).
+struct Table {
+  float d[3][64];              // offsets from the chunk's first token along each axis
+  float4 group[16];            // the same for rows 4g (t, h, w)
+  unsigned long long below[3][68];  // rows whose offset along the axis is below v, v = 0 .. box extent
 };
-__device__ __forceinline__ void fill_coltab(const Geom& g, ColTab* tab, int r) {
-  const uint32_t c = chunk_row_code(g, r);
-  tab->d[0][r] = (float)(c & 0xffu);
-  tab->d[1][r] = (float)((c >> 8) & 0xffu);
-  tab->d[2][r] = (float)((c >> 16) & 0xffu);
+// Filled by all NT threads; codes of the rows in colc (shared, visible).
+template <int NT>
+__device__ __forceinline__ void fill_table(const Geom& g, Table* tab, const uint32_t* colc) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 64) {
+    const uint32_t c = colc[tid];
+    const float4 d = make_float4((float)(c & 0xffu), (float)((c >> 8) & 0xffu), (float)((c >> 16) & 0xffu), 0.f);
+    tab->d[0][tid] = d.x;
+    tab->d[1][tid] = d.y;
+    tab->d[2][tid] = d.z;
+    if (tid % 4 == 0) tab->group[tid / 4] = d;
+  }
+  const int n0 = g.ct + 1, n1 = n0 + g.ch + 1, n2 = n1 + g.cw + 1;
+  const uint32_t ca = colc[lane], cb = colc[lane + 32];
+  for (int e = tid / 32; e < n2; e += NT / 32) {
+    const int a = e < n0 ? 0 : e < n1 ? 1 : 2, v = e - (a == 0 ? 0 : a == 1 ? n0 : n1);
+    const uint32_t lo = __ballot_sync(0xffffffffu, (int)((ca >> (8 * a)) & 0xffu) < v);
+    const uint32_t hi = __ballot_sync(0xffffffffu, (int)((cb >> (8 * a)) & 0xffu) < v);
+    if (lane == 0) tab->below[a][v] = ((unsigned long long)hi << 32) | lo;
+  }
+}
+
+// Which rows of a chunk a token sees by coordinates: offset along t in
+// [lo, vt), along h and w below vh and vw (any integers).
+__device__ __forceinline__ unsigned long long visible_box(const Geom& g, const Table* tab, int lo, int vt, int vh, int vw) {
+  return tab->below[0][min(max(vt, 0), g.ct)] & ~tab->below[0][min(max(lo, 0), g.ct)] &
+         tab->below[1][min(max(vh, 0), g.ch)] & tab->below[2][min(max(vw, 0), g.cw)];
+}
+
+// Which rows of a chunk carry the token's id.
+__device__ __forceinline__ unsigned long long visible_doc(const ModParams& m, size_t chunk, int id) {
+  const DocChunk* c = m.doc_chunks + chunk;
+  const int4 ids = __ldg(&c->id);
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(c->rows)), b = __ldg(reinterpret_cast<const ulonglong2*>(c->rows + 2));
+  unsigned long long vis = (ids.x == id ? a.x : 0ull) | (ids.y == id ? a.y : 0ull) | (ids.z == id ? b.x : 0ull);
+  if (ids.w != kManyIds) return vis | (ids.w == id ? b.y : 0ull);
+  // More than four ids in 64 tokens: the rows themselves.
+  const int4* d4 = reinterpret_cast<const int4*>(m.doc_rows + 64 * chunk);
+  vis = 0;
+  for (int q = 0; q < 16; ++q) {
+    const int4 d = __ldg(d4 + q);
+    vis |= (unsigned long long)((d.x == id ? 1u : 0u) | (d.y == id ? 2u : 0u) | (d.z == id ? 4u : 0u) | (d.w == id ? 8u : 0u)) << (4 * q);
+  }
+  return vis;
 }
 
 // y[q] += sum over the axes of nw[a] |at[a] - d[a][first + q]|: the distance
-// bias of a token at offset `at` from the chunk's first token, or, with
-// y = 0 and positive weights, the distance itself. Axes of weight zero are
+// bias of a token at offset `at` from the chunk's first token, or, with y = 0
+// and positive weights, the distance itself. In chunks whose rows of four lie
+// along w (cw a multiple of 4) the t and h terms are one value for four
+// columns, and cw = 4 leaves four w terms per step: 3 operations a column
+// against 6.75 for axis after axis. Axes of weight zero or of one token are
 // passed over.
 template <int N>
-__device__ __forceinline__ void add_distance(float* y, const ColTab* tab, int first, const float* at, const float* nw) {
+__device__ __forceinline__ void add_distance(const Geom& g, float* y, const Table* tab, int first, const float* at,
+                                             const float* nw) {
+  if (g.cw % 4 == 0) {
+    const bool along_w = nw[2] != 0.f && g.W > 1;
+    float cw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cw[i] = nw[2] * fabsf(at[2] - (float)i);
+    if (g.cw == 4 && along_w) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const float4 d = tab->group[first / 4 + q];
+        const float u = fmaf(nw[1], fabsf(at[1] - d.y), nw[0] * fabsf(at[0] - d.x));
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 r = __fadd2_rn(make_float2(y[4 * q + i], y[4 * q + i + 1]), __fadd2_rn(bc(u), make_float2(cw[i], cw[i + 1])));
+          y[4 * q + i] = r.x;
+          y[4 * q + i + 1] = r.y;
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 d = tab->group[first / 4 + q];
+      const float u = fmaf(nw[1], fabsf(at[1] - d.y), nw[0] * fabsf(at[0] - d.x));
+      const float w = at[2] - d.z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[4 * q + i] += u;
+        if (along_w) y[4 * q + i] = fmaf(nw[2], fabsf(w - (float)i), y[4 * q + i]);
+      }
+    }
+    return;
+  }
+  const int extent[3] = {g.T, g.H, g.W};
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
-    if (nw[a] == 0.f) continue;
+    if (nw[a] == 0.f || extent[a] == 1) continue;
     const float4* d4 = reinterpret_cast<const float4*>(tab->d[a] + first);
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) {
@@ -217,30 +309,6 @@ __device__ __forceinline__ void add_distance(float* y, const ColTab* tab, int fi
       y[4 * q + 3] = fmaf(fabsf(at[a] - d.w), nw[a], y[4 * q + 3]);
     }
   }
-}
-
-// Which of 32 columns (rows first .. of the chunk whose codes colc holds) a
-// row sees: offset along t in [lo, vt), along h and w below vh and vw, and,
-// where docs is given (the chunk's ids in row order), the row's id.
-__device__ __forceinline__ uint32_t visible32(const uint32_t* colc, int first, int lo, int vt, int vh, int vw,
-                                              const int32_t* docs, int id) {
-  uint32_t vis = 0;
-#pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    const uint32_t cc = colc[first + q];
-    const int t = (int)(cc & 0xffu);
-    vis |= (t >= lo && t < vt && (int)((cc >> 8) & 0xffu) < vh && (int)((cc >> 16) & 0xffu) < vw ? 1u : 0u) << q;
-  }
-  if (docs) {
-    const int4* d4 = reinterpret_cast<const int4*>(docs + first);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int4 d = __ldg(d4 + q);
-      const uint32_t same = (d.x == id ? 1u : 0u) | (d.y == id ? 2u : 0u) | (d.z == id ? 4u : 0u) | (d.w == id ? 8u : 0u);
-      vis &= ~((~same & 0xFu) << (4 * q));
-    }
-  }
-  return vis;
 }
 
 // Zeroes a 64-row operand tile's rows of hidden tokens (128-byte swizzle: a
