@@ -36,8 +36,8 @@
 // dK more than all other roundings where the softmax is sharp. In a row of
 // probabilities eps_i = sum_j P_ij (dP_ij - Delta_i), so the kernel sums that
 // next to a second accumulator G_i = sum_j P_ij (1 - tanh^2) K_j (one more
-// product a step) and writes dQ_i = scale (dQ_i - eps_i G_i) and Delta_i +
-// eps_i, which dK then reads.
+// product a step) and writes dQ_i = scale (dQ_i - eps_i G_i) and -(Delta_i +
+// eps_i), which the dK pass then reads.
 //
 // Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased
 // and masked scores; the step lists are filtered as in the forward. Hidden
@@ -45,6 +45,8 @@
 // of hidden tokens in a step's tiles are zeroed in shared memory before the
 // product that sums over them.
 #include <cudaTypedefs.h>
+
+#include <math.h>
 
 #include <type_traits>
 
@@ -98,7 +100,8 @@ struct DqParams {
 
 struct DqParamsMod : DqParams {
   ModParams mod;
-  float* delta_out;    // delta, corrected
+  float* neg_delta;    // gets -(Delta + eps) of every row, 0 where no gradient passes
+  float* neg_lse2;     // gets -lse log2(e) of every row, -inf where no gradient passes
   float* slope_parts;  // null, or [B * heads, CTAs per head]: the slope gradient's parts
 };
 
@@ -449,9 +452,15 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const float c = P.scale_log2;
     bool ok = true;
     mod::Row row{};
-    float slope = 0.f, sw = 0.f, swd = 0.f, spd = 0.f;  // sums of w = P (dP - Delta), w dist, P dist
+    float slope = 0.f;
+    float2 sw2 = mod::bc(0.f), swd2 = sw2, spd2 = sw2;  // sums of w = P (dP - Delta), w dist, P dist
+    float nlse2 = -lse2, ndlt = -dlt;
     if constexpr (MOD) {
       if (row_exists) row = mod::row_of(g, P.mod, b, half ? i1 : i0, half ? c1 : c0, colc[r & 63], r & 63);
+      if (!row.live || nlse2 == INFINITY) {  // no key seen: P = 0
+        nlse2 = -INFINITY;
+        ndlt = 0.f;
+      }
       if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
     }
     for (int n = 0; n < L; ++n) {
@@ -490,52 +499,51 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             vis = (uint32_t)(all >> (32 * part));
           }
           uint32_t sr[32], pr[32];
-          tc::tmem_ld32_wait(sbuf, sr);
-          tc::tmem_ld32_wait(pbuf, pr);
-          // y = log2 of P: raw scores (or tanh values) times c2, bias, minus the log-sum-exp.
+          tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
+          // log2 of P = raw scores (or tanh values) times c2, bias, minus the log-sum-exp.
           float c2 = c;
-          const bool cap = M.cap > 0.f;
-          if (cap) {
+          if (M.cap > 0.f) {
             mod::tanh_scores<32>(sr, P.scale / M.cap);
             c2 = M.cap * mod::kLog2e;
           }
           float far[32];
-#pragma unroll
-          for (int q = 0; q < 32; ++q) far[q] = 0.f;
           if (M.slopes) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) far[q] = 0.f;
             const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
             mod::add_distance<32>(g, far, &tab->col, 32 * part, at, M.dist);
           }
-          const float s2 = -slope * mod::kLog2e;
-          auto form = [&](auto masked) {
+          const float2 cc2 = mod::bc(c2), ss2 = mod::bc(-slope * mod::kLog2e), nl2 = mod::bc(nlse2), nd2 = mod::bc(ndlt);
+          auto form = [&](auto masked, auto cap, auto bias) {
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              float d2[2], g2[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int x = 2 * q + u;
-                const float th = __uint_as_float(sr[x]);
-                float p = tc::ex2(fmaf(far[x], s2, fmaf(th, c2, -lse2)));
-                float w = p * (__uint_as_float(pr[x]) - dlt);
-                if (masked && !((vis >> x) & 1u)) p = w = 0.f;
-                sw += w;
-                if (P.slope_parts) {
-                  swd = fmaf(w, far[x], swd);
-                  spd = fmaf(p, far[x], spd);
-                }
-                const float gain = cap ? fmaf(-th, th, 1.f) : 1.f;
-                d2[u] = masked && cap && !((vis >> x) & 1u) ? 0.f : w * gain;
-                g2[u] = masked && cap && !((vis >> x) & 1u) ? 0.f : p * gain;
+              float2 th = mod::pair(sr + 2 * q), dp = mod::pair(pr + 2 * q);
+              const bool v0 = (vis >> (2 * q)) & 1u, v1 = (vis >> (2 * q + 1)) & 1u;
+              if (masked) {  // whatever hidden rows left in S and dP
+                th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
+                dp = make_float2(v0 ? dp.x : 0.f, v1 ? dp.y : 0.f);
               }
-              __nv_bfloat162 hv = __floats2bfloat162_rn(d2[0], d2[1]), hg = __floats2bfloat162_rn(g2[0], g2[1]);
-              dsw[q] = *reinterpret_cast<uint32_t*>(&hv);
-              gw[q] = *reinterpret_cast<uint32_t*>(&hg);
+              float2 y = __ffma2_rn(th, cc2, nl2);
+              const float2 d = bias ? make_float2(far[2 * q], far[2 * q + 1]) : mod::bc(0.f);
+              if (bias) y = __ffma2_rn(d, ss2, y);
+              float2 p = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+              if (masked) p = make_float2(v0 ? p.x : 0.f, v1 ? p.y : 0.f);
+              float2 w = __fmul2_rn(p, __fadd2_rn(dp, nd2));
+              sw2 = __fadd2_rn(sw2, w);
+              if (bias) {
+                swd2 = __ffma2_rn(w, d, swd2);
+                spd2 = __ffma2_rn(p, d, spd2);
+              }
+              if (cap) {
+                const float2 gain = __ffma2_rn(make_float2(-th.x, -th.y), th, mod::bc(1.f));
+                w = __fmul2_rn(w, gain);
+                p = __fmul2_rn(p, gain);
+              }
+              dsw[q] = mod::pack(w);
+              gw[q] = mod::pack(p);
             }
           };
-          if (__all_sync(0xffffffffu, vis == 0xffffffffu))
-            form(std::false_type{});
-          else
-            form(std::true_type{});
+          mod::dispatch(!__all_sync(0xffffffffu, vis == 0xffffffffu), M.cap > 0.f, M.slopes != nullptr, form);
         }
       } else if (!MOD && keep) {
         const uint32_t ext = uext[n];
@@ -592,6 +600,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // The two halves' sums. With w = P (dP - Delta) for any Delta and sum P
       // = 1: eps = sum w, and the row's share of -sum dZ dist is eps (sum P
       // dist) - sum w dist.
+      const float sw = sw2.x + sw2.y, swd = swd2.x + swd2.y, spd = spd2.x + spd2.y;
       float* red = reinterpret_cast<float*>(smem + C::OFF_V);  // the V ring is no longer read
       const bool use = ok && L > 0;
       if (use) {
@@ -601,13 +610,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
       float v = 0.f;
-      if (use && row.live) {
-        const int o = 3 * (tid ^ 128);
-        eps = sw + red[o];
-        if (part == 0) {
-          P.delta_out[lrow] = dlt + eps;
-          v = eps * (spd + red[o + 2]) - (swd + red[o + 1]);
-        }
+      const int o = 3 * (tid ^ 128);
+      if (use && row.live) eps = sw + red[o];
+      if (part == 0 && row_exists) {
+        P.neg_delta[lrow] = ndlt - eps;
+        P.neg_lse2[lrow] = nlse2;
+        if (use && row.live) v = eps * (spd + red[o + 2]) - (swd + red[o + 1]);
       }
       if (P.slope_parts) {
 #pragma unroll
@@ -714,8 +722,8 @@ struct KvParams {
   Geom g;
   const int32_t* idxT;  // [B, Hh, N, N] query tiles keeping each key tile, ascending
   const int32_t* cntT;  // [B, Hh, N]
-  const float* lse;
-  const float* delta;
+  const float* lse;    // with score rules: -lse log2(e)
+  const float* delta;  // with score rules: -Delta
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   float scale;
@@ -1032,45 +1040,45 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             vis = (uint32_t)(all >> (32 * part));
           }
           uint32_t sr[32], pr[32];
-          tc::tmem_ld32_wait(sbuf, sr);
-          tc::tmem_ld32_wait(pbuf, pr);
+          tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
           float c2 = c;
-          const bool cap = M.cap > 0.f;
-          if (cap) {
+          if (M.cap > 0.f) {
             mod::tanh_scores<32>(sr, P.scale / M.cap);
             c2 = M.cap * mod::kLog2e;
           }
-          float y[32];
+          float y[32];  // -lse log2(e) of the queries, plus the bias
 #pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] = fmaf(__uint_as_float(sr[q]), c2, -ld[32 * part + q] * mod::kLog2e);
+          for (int q = 0; q < 8; ++q) *reinterpret_cast<float4*>(y + 4 * q) = reinterpret_cast<const float4*>(ld + 32 * part)[q];
           if (M.slopes) {
             const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
             const float s2 = -slope * mod::kLog2e;
             const float nw[3] = {s2 * M.dist[0], s2 * M.dist[1], s2 * M.dist[2]};
             mod::add_distance<32>(g, y, &tab->col, 32 * part, at, nw);
           }
-          auto form = [&](auto masked) {
+          const float2 cc2 = mod::bc(c2);
+          auto form = [&](auto masked, auto cap, auto) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              float pp[2], d2[2];
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const float4 nd = reinterpret_cast<const float4*>(ld + 64 + 32 * part)[q4];  // -Delta of four queries
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int x = 2 * q + u;
-                const float th = __uint_as_float(sr[x]);
-                pp[u] = tc::ex2(y[x]);
-                d2[u] = pp[u] * (__uint_as_float(pr[x]) - ld[64 + 32 * part + x]);
-                if (cap) d2[u] *= fmaf(-th, th, 1.f);
-                if (masked && !((vis >> x) & 1u)) pp[u] = d2[u] = 0.f;
+              for (int q = 2 * q4; q < 2 * q4 + 2; ++q) {
+                float2 th = mod::pair(sr + 2 * q), dp = mod::pair(pr + 2 * q);
+                const bool v0 = (vis >> (2 * q)) & 1u, v1 = (vis >> (2 * q + 1)) & 1u;
+                if (masked) {
+                  th = make_float2(v0 ? th.x : 0.f, v1 ? th.y : 0.f);
+                  dp = make_float2(v0 ? dp.x : 0.f, v1 ? dp.y : 0.f);
+                }
+                const float2 e = __ffma2_rn(th, cc2, make_float2(y[2 * q], y[2 * q + 1]));
+                float2 p = make_float2(tc::ex2(e.x), tc::ex2(e.y));
+                if (masked) p = make_float2(v0 ? p.x : 0.f, v1 ? p.y : 0.f);
+                pw[q] = mod::pack(p);
+                float2 w = __fmul2_rn(p, __fadd2_rn(dp, q & 1 ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
+                if (cap) w = __fmul2_rn(w, __ffma2_rn(make_float2(-th.x, -th.y), th, mod::bc(1.f)));
+                dw[q] = mod::pack(w);
               }
-              __nv_bfloat162 hp = __floats2bfloat162_rn(pp[0], pp[1]), hd = __floats2bfloat162_rn(d2[0], d2[1]);
-              pw[q] = *reinterpret_cast<uint32_t*>(&hp);
-              dw[q] = *reinterpret_cast<uint32_t*>(&hd);
             }
           };
-          if (__all_sync(0xffffffffu, vis == 0xffffffffu))
-            form(std::false_type{});
-          else
-            form(std::true_type{});
+          mod::dispatch(!__all_sync(0xffffffffu, vis == 0xffffffffu), M.cap > 0.f, false, form);
         }
       } else if (!MOD && keep) {
         const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
@@ -1220,7 +1228,7 @@ static bool fits(const P& prm) {
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod,
-                                    float* slope_parts) {
+                                    float* neg_lse2, float* slope_parts) {
   DqParamsMod prm;
   prm.g = make_geom(p);
   prm.idx = idx;
@@ -1241,7 +1249,8 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
   const bool d128 = p->desc.head_dim == 128;
   if (mod) {
     prm.mod = *mod;
-    prm.delta_out = delta;
+    prm.neg_delta = delta;
+    prm.neg_lse2 = neg_lse2;
     prm.slope_parts = slope_parts;
     if (d128)
       return fits<DqCfg<128, true, 4>>(prm) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)

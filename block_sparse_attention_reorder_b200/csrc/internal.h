@@ -209,14 +209,15 @@ struct BackwardWs {
 bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* o,
                               const void* d_o, const float* lse, const int32_t* idx, const int32_t* cnt, void* dq,
                               void* dk, void* dv, const BackwardWs& w, cudaStream_t st,
-                              const ModParams* mod = nullptr, float* slope_parts = nullptr);
+                              const ModParams* mod = nullptr, float* neg_lse2 = nullptr, float* slope_parts = nullptr);
 
 // dQ of the backward on the tensor cores (tiled bf16 q, k, v, dO; lse and
-// rowsum(dO * O) tiled fp32; with score rules delta is corrected in place).
+// rowsum(dO * O) tiled fp32; with score rules delta becomes the negative of the corrected one, and
+// neg_lse2 [B, Hh, N, V] gets -lse log2(e): what the dK, dV pass then takes for delta and lse).
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod = nullptr,
-                                    float* slope_parts = nullptr);
+                                    float* neg_lse2 = nullptr, float* slope_parts = nullptr);
 
 // dK and dV of the backward on the tensor cores, over the transposed lists.
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,

@@ -38,6 +38,7 @@ DocWs carve_doc(const bsattn_plan* p, Carve& c) {
 struct BwdModWs {
   DocWs doc;
   float* slope_parts;
+  float* neg_lse2;
   BackwardWs b;
 };
 BwdModWs carve_backward_mod(const bsattn_plan* p, Carve& c) {
@@ -45,6 +46,7 @@ BwdModWs carve_backward_mod(const bsattn_plan* p, Carve& c) {
   BwdModWs w;
   w.doc = carve_doc(p, c);
   w.slope_parts = (float*)c.take((size_t)p->desc.B * p->desc.heads * attention_items(p) * sizeof(float));
+  w.neg_lse2 = (float*)c.take(rows * p->V * sizeof(float));
   w.b.delta = (float*)c.take(rows * p->V * sizeof(float));
   w.b.bm = (uint32_t*)c.take(rows * ((p->N + 31) / 32) * sizeof(uint32_t));
   w.b.idxT = (int32_t*)c.take(rows * p->N * sizeof(int32_t));
@@ -391,7 +393,7 @@ bsattn_status attn_backward_mod(const bsattn_plan* p, const bsattn_score_mod* m,
   const BwdModWs w = carve_backward_mod(p, c);
   if ((s = launch_doc_prep(p, m, w.doc, st))) return s;
   const ModParams d = device_mod(p, m, w.doc);
-  if ((s = launch_backward(p, q, k, v, o, d_o, lse, idx, cnt, dq, dk, dv, w.b, st, &d,
+  if ((s = launch_backward(p, q, k, v, o, d_o, lse, idx, cnt, dq, dk, dv, w.b, st, &d, w.neg_lse2,
                            d_slopes ? w.slope_parts : nullptr)))
     return s;
   if (!d_slopes) return BSATTN_OK;

@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "tc_common.cuh"
 
@@ -20,6 +22,25 @@ constexpr int kHiddenDoc = -2;  // a query id that equals no key's
 // FMA-pipe operations on packed pairs, the SFU stays free for the softmax.
 constexpr float kSmall = 0.75f, kTiny = 0.375f;
 __device__ __forceinline__ float2 bc(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const uint32_t* r) { return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+__device__ __forceinline__ uint32_t pack(float2 v) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+// f(a, b, c) with the three conditions (uniform over the warp) as constants,
+// so that one straight loop runs per step.
+template <class F>
+__device__ __forceinline__ void dispatch(bool a, bool b, bool c, F&& f) {
+  constexpr std::true_type Y{};
+  constexpr std::false_type N{};
+  if (a) {
+    if (b) c ? f(Y, Y, Y) : f(Y, Y, N);
+    else c ? f(Y, N, Y) : f(Y, N, N);
+  } else {
+    if (b) c ? f(N, Y, Y) : f(N, Y, N);
+    else c ? f(N, N, Y) : f(N, N, N);
+  }
+}
 __device__ __forceinline__ float2 tanh_tiny2(float2 u) {
   const float2 v = __fmul2_rn(u, u);
   float2 p = __ffma2_rn(bc(-0.04848729074001312f), v, bc(0.1328972578048706f));
