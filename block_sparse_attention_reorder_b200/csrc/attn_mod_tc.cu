@@ -1,0 +1,659 @@
+// Block-sparse attention forward under score rules (tanh cap, distance bias,
+// causal, prefix and document masks) on the 5th-generation tensor cores.
+//
+// Work unit, step list, rings and TMEM layout are those of the forward
+// without rules (csrc/attn_tc.cu): a 128-row query block of two 64-row chunks
+// walks the union of their kept key chunks, S = Q K^T (N = 64) and O += P V
+// per step, two CTAs per SM. Different is what stands between the products:
+//
+//  * The step list is filtered by the rules at set-up (score_mod.cuh): chunks
+//    hidden from the whole block are never loaded, and only steps that need
+//    element masks evaluate them, from shared bit tables.
+//  * The rules cost 3 to 10 FMA-pipe operations a score on top of the
+//    softmax's four; masks and their tables are fetched while S is computed.
+//  * The reference m of 2^(x - m) is set by the first step that shows the row
+//    a key and moves only when a score grows by more than 2^100, for which
+//    fp32's exponent range has room in the sums and in bf16 P. So no step
+//    waits for its row maximum: the step's sum shows whether a term was too
+//    large, and then, hardly ever, the step is taken again with the maximum,
+//    and O rescaled.
+//
+// Roles (192 threads): warps 0-3 rules and softmax (thread r owns query row r),
+// warp 4 TMA producer, warp 5 MMA issuer. Every mbarrier wait is bounded; on expiry the CTA sets the
+// device error word, lets issued copies land, drains its MMAs and frees TMEM.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "internal.h"
+#include "score_mod.cuh"
+#include "steps.cuh"
+#include "tc_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kStages = 2;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColS0 = 0, kColS1 = 64, kColO = 128;
+constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
+constexpr long long kTestWaitLimit = 2000000LL;  // ~1 ms, with the testing hook on
+// A row's reference m is put kAbove over a maximum and stays until a score
+// exceeds m by kRaise (log2 units): probabilities between 2^-40 and 2^60
+// times their rounding are exact in fp32 sums and bf16 alike, and terms that
+// fall below fp32's range are under 2^-86 of the largest.
+constexpr float kAbove = 40.f, kRaise = 60.f;
+constexpr float kSumLimit = 0x1p60f;  // no term of a smaller sum exceeds m + kRaise
+
+struct Params {
+  Geom g;
+  ModParams mod;
+  const float* qs;
+  const float* ks;
+  const int32_t* idx;
+  const int32_t* cnt;
+  int kmax;
+  __nv_bfloat16* o;
+  float* lse;
+  float scale;
+  int* err;
+  int umax;      // step list capacity
+  int bm_words;  // bitmap words per list
+  int pair_axis;
+  int pdim[3];
+  long long wait_limit;
+  int stall;  // testing: the MMA thread first waits on a barrier nothing arrives at
+};
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int QRB = D * ESZ;        // Q/K row bytes
+  static constexpr int SWB = QRB >= 128 ? 128 : 64;
+  static constexpr uint32_t LAYOUT = SWB == 128 ? tc::kLayoutSW128 : tc::kLayoutSW64;
+  static constexpr int QBLK = QRB / SWB;     // column blocks of Q/K
+  static constexpr int NKS = QRB / 32;       // S MMAs (32 bytes of K each)
+  static constexpr int KS_PER_BLK = SWB / 32;
+  static constexpr int K_BYTES = 64 * QRB;
+  static constexpr int V_BYTES = 64 * D * 2;
+  static constexpr int VBLK = D / 64;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 128 * QRB;
+  static constexpr int OFF_V = OFF_K + kStages * K_BYTES;
+  static constexpr int OFF_BAR = OFF_V + kStages * V_BYTES;
+  // barriers: q, kfull[S], vfull[S], sfull[2], pfull[2], pvdone[2], final
+  static constexpr int NBAR = 1 + 2 * kStages + 7;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort, steps, zero
+  static constexpr int OFF_COL = OFF_MISC + 16;        // 64 packed row codes
+  static constexpr int OFF_SCAN = OFF_COL + 256;
+  static constexpr int OFF_TOK = OFF_SCAN + 64;        // epilogue: natural token of each block row
+  static constexpr int OFF_TAB = OFF_TOK + 512;
+  static constexpr int OFF_DYN = OFF_TAB + (int)sizeof(ModTab);  // bitmaps, step list, coordinates
+  static constexpr int O_PITCH = D * 2 + 16;
+  static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
+  static_assert(128 * O_PITCH <= OFF_BAR - OFF_K, "epilogue staging fits in the rings");
+};
+
+__device__ __forceinline__ void record_timeout(volatile int* abort_flag, int* err) {
+  *abort_flag = 1;
+  atomicOr(err, BSATTN_DEVERR_TIMEOUT);
+}
+
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// CAP and BIAS: whether scores are capped and biased. Masks need no variant:
+// steps that need none skip them by one flag test. Branches and scalar work
+// per step are what a softmax warp cannot hide (two divisions a step cost
+// 20% of the time), so what the call fixes is fixed at compile time or ahead
+// of the loop.
+template <int D, bool FP8, bool NAT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params P) {
+  using C = Cfg<D, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = tc::smem_addr(smem);
+  const uint32_t bar_q = sb + C::OFF_BAR;
+  auto bar_kfull = [&](int s) { return sb + C::OFF_BAR + 8u * (1 + s); };
+  auto bar_vfull = [&](int s) { return sb + C::OFF_BAR + 8u * (1 + kStages + s); };
+  auto bar_sfull = [&](int b) { return sb + C::OFF_BAR + 8u * (1 + 2 * kStages + b); };
+  auto bar_pfull = [&](int b) { return sb + C::OFF_BAR + 8u * (3 + 2 * kStages + b); };
+  auto bar_pvdone = [&](int b) { return sb + C::OFF_BAR + 8u * (5 + 2 * kStages + b); };
+  const uint32_t bar_final = sb + C::OFF_BAR + 8u * (7 + 2 * kStages);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* never = reinterpret_cast<volatile int*>(misc + 3);  // stays 0: waits that ignore abort
+  uint32_t* colc = reinterpret_cast<uint32_t*>(smem + C::OFF_COL);
+  int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  ModTab* tab = reinterpret_cast<ModTab*>(smem + C::OFF_TAB);
+  uint32_t* bmA = reinterpret_cast<uint32_t*>(smem + C::OFF_DYN);
+  uint32_t* bmB = bmA + P.bm_words;
+  uint32_t* ulist = bmB + P.bm_words;
+  uint32_t* uext = ulist + P.umax;                        // packed coordinates and flags of each step
+  float* uks = reinterpret_cast<float*>(uext + P.umax);   // e4m3: each step's key-tile scale
+
+  const Geom& g = P.g;
+  const ModParams& M = P.mod;
+  int i0, i1, c0, c1;
+  block_halves(g, P.pair_axis, P.pdim, blockIdx.x, &i0, &i1, &c0, &c1);
+  if (NAT && g.nchunk > 1) {  // chunks of padded rows only are never written to the natural layout
+    if (i1 >= 0 && !chunk_is_real(g, i1, c1)) i1 = -1;
+    if (!chunk_is_real(g, i0, c0)) {
+      if (i1 < 0) return;  // uniform over the CTA, before any setup
+      c0 = c1;
+      i1 = -1;
+    }
+  }
+  const int head = blockIdx.y, b = blockIdx.z;
+  const size_t bh = (size_t)b * g.Hh + head;
+  const bool has1 = i1 >= 0;
+  // First tiled-layout row of chunk c of tile j.
+  auto tiled_row = [&](int j, int c) -> int { return (int)((bh * g.N + j) * g.V) + 64 * c; };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // The list counts and this thread's first entry of each list come first, so
+  // that their latency overlaps the set-up (entries at and beyond a count are
+  // read but not used).
+  const int32_t* lA = P.idx + (bh * g.N + i0) * (size_t)P.kmax;
+  const int32_t* lB = has1 ? P.idx + (bh * g.N + i1) * (size_t)P.kmax : lA;
+  int nA = P.cnt[bh * g.N + i0];
+  int nB = has1 ? P.cnt[bh * g.N + i1] : 0;
+  int jA = tid < P.kmax ? __ldg(lA + tid) : 0;
+  int jB = has1 && tid < P.kmax ? __ldg(lB + tid) : 0;
+
+  // ------------------------------------------------------------ setup
+  if (tid == 0) {
+    tc::mbar_init(bar_q, 1);
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(bar_kfull(s), 1);
+      tc::mbar_init(bar_vfull(s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(bar_sfull(x), 1);
+      tc::mbar_init(bar_pfull(x), kSoftmaxThreads);
+      tc::mbar_init(bar_pvdone(x), 1);
+    }
+    tc::mbar_init(bar_final, 1);
+    misc[1] = 0;
+    misc[3] = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(sb + C::OFF_MISC, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (tid < 64) colc[tid] = chunk_row_code(g, tid);
+  if (g.cr < 64) {
+    // Tiles of fewer than 64 tokens: natural-layout loads fill only the
+    // chunk box's rows; the rest of every V slot must hold finite values.
+    for (int x = tid; x < kStages * C::V_BYTES / 16; x += kThreads)
+      reinterpret_cast<uint4*>(smem + C::OFF_V)[x] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  for (int w = tid; w < 2 * P.bm_words; w += kThreads) bmA[w] = 0u;
+  if (!has1) {  // rows 64..127 of the query block have no chunk
+    for (int x = tid; x < C::QBLK * 64 * C::SWB / 16; x += kThreads) {
+      const int cb = x / (64 * C::SWB / 16), off = x % (64 * C::SWB / 16);
+      reinterpret_cast<uint4*>(smem + C::OFF_Q + cb * 128 * C::SWB + 64 * C::SWB)[off] = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  const int prefix = M.prefix ? __ldg(M.prefix + b) : 0;
+  __syncthreads();
+  if (nA < 0 || nA > P.kmax || nB < 0 || nB > P.kmax) {
+    if (tid == 0) atomicOr(P.err, BSATTN_DEVERR_BAD_INDEX);
+    nA = min(max(nA, 0), P.kmax);
+    nB = min(max(nB, 0), P.kmax);
+  }
+  {
+    for (int e = tid; e < max(nA, nB); e += kThreads) {
+      if (e != tid) {
+        jA = e < nA ? __ldg(lA + e) : 0;
+        jB = e < nB ? __ldg(lB + e) : 0;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (e >= (x ? nB : nA)) continue;
+        const int j = x ? jB : jA;
+        if (j < 0 || j >= g.N) {
+          atomicOr(P.err, BSATTN_DEVERR_BAD_INDEX);
+          continue;
+        }
+        atomicOr(x ? &bmB[j >> 5] : &bmA[j >> 5], 1u << (j & 31));
+      }
+    }
+  }
+  __syncthreads();
+  compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
+  fill_modtab<kThreads>(g, tab, colc);
+  __syncthreads();
+  {
+    const int steps = (int)misc[2];
+    const int left = mod::filter_steps<kThreads, false>(g, M, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
+    __syncthreads();
+    if (tid == 0) misc[2] = (uint32_t)left;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = misc[0];
+  const int L = (int)misc[2];
+
+  // ------------------------------------------------------------ roles
+  if (warp == 4) {
+    if (lane == 0 && L > 0) {
+      tc::tma_prefetch_desc(&tmQ);
+      tc::tma_prefetch_desc(&tmK);
+      tc::tma_prefetch_desc(&tmV);
+      // A natural-layout load fills the chunk box's rows (cr of them).
+      const int qrows = NAT && !FP8 ? g.cr : 64, kvrows = NAT ? g.cr : 64;
+      // One chunk (64 tokens x 64 columns) of a natural-layout tensor: the
+      // box {64 columns, cw, ch, ct, 1} at the chunk's first token.
+      auto load_nat = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, mod::Coord p) {
+        tc::tma_load_5d(dst, map, bar, col, p.w, p.h, p.t, b);
+      };
+      tc::mbar_arrive_expect_tx(bar_q, (has1 ? 2 : 1) * qrows * C::QRB);
+      for (int x = 0; x < (has1 ? 2 : 1); ++x) {
+        const int tile = x ? i1 : i0, chunk = x ? c1 : c0;
+        const mod::Coord qp = mod::chunk_first(g, M, mod::pack_tile(g, M, tile), chunk_origin(g, chunk));
+#pragma unroll
+        for (int cb = 0; cb < C::QBLK; ++cb) {
+          const uint32_t dst = sb + C::OFF_Q + cb * 128 * C::SWB + x * 64 * C::SWB;
+          if (NAT && !FP8)
+            load_nat(dst, &tmQ, bar_q, head * D + cb * 64, qp);
+          else
+            tc::tma_load_2d(dst, &tmQ, bar_q, cb * C::SWB / C::ESZ, tiled_row(tile, chunk));
+        }
+      }
+      // K_m is issued as soon as S_{m-2} has released its slot, V_{m-1} once
+      // PV_{m-3} has: K runs one step ahead of V.
+      int lastk[kStages], lastv[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) lastk[s] = lastv[s] = -1;
+      for (int m = 0; m <= L; ++m) {
+        if (m < L) {
+          const int s = m % kStages;
+          if (m >= kStages &&
+              !tc::mbar_wait(bar_sfull(s), ((m / kStages) - 1) & 1, abort_flag, P.wait_limit)) {
+            record_timeout(abort_flag, P.err);
+            break;
+          }
+          const int kt = (int)(ulist[m] & 0x1FFFFFu), kc = (int)((ulist[m] >> 21) & 0x1FFu);
+          tc::mbar_arrive_expect_tx(bar_kfull(s), FP8 ? C::K_BYTES : kvrows * C::QRB);
+          const mod::Coord kp = mod::chunk_first(g, M, uext[m], tab->at(kc));
+#pragma unroll
+          for (int cb = 0; cb < C::QBLK; ++cb) {
+            const uint32_t dst = sb + C::OFF_K + s * C::K_BYTES + cb * 64 * C::SWB;
+            if (NAT && !FP8)
+              load_nat(dst, &tmK, bar_kfull(s), head * D + cb * 64, kp);
+            else
+              tc::tma_load_2d(dst, &tmK, bar_kfull(s), cb * C::SWB / C::ESZ, tiled_row(kt, kc));
+          }
+          lastk[s] = m;
+        }
+        if (m >= 1) {
+          const int v = m - 1, s = v % kStages;
+          if (v >= kStages &&
+              !tc::mbar_wait(bar_pvdone(s), ((v / kStages) - 1) & 1, abort_flag, P.wait_limit)) {
+            record_timeout(abort_flag, P.err);
+            break;
+          }
+          const int vt = (int)(ulist[v] & 0x1FFFFFu), vc = (int)((ulist[v] >> 21) & 0x1FFu);
+          tc::mbar_arrive_expect_tx(bar_vfull(s), kvrows * D * 2);
+          const mod::Coord vp = mod::chunk_first(g, M, uext[v], tab->at(vc));
+#pragma unroll
+          for (int vb = 0; vb < C::VBLK; ++vb) {
+            const uint32_t dst = sb + C::OFF_V + s * C::V_BYTES + vb * 8192;
+            if (NAT)
+              load_nat(dst, &tmV, bar_vfull(s), head * D + vb * 64, vp);
+            else
+              tc::tma_load_2d(dst, &tmV, bar_vfull(s), vb * 64, tiled_row(vt, vc));
+          }
+          lastv[s] = v;
+        }
+      }
+      if (*abort_flag) {
+        // Let copies already issued land before the CTA's memory goes away.
+        tc::mbar_wait(bar_q, 0, never, kWaitLimit);
+        for (int s = 0; s < kStages; ++s) {
+          if (lastk[s] >= 0) tc::mbar_wait(bar_kfull(s), (lastk[s] / kStages) & 1, never, kWaitLimit);
+          if (lastv[s] >= 0) tc::mbar_wait(bar_vfull(s), (lastv[s] / kStages) & 1, never, kWaitLimit);
+        }
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0 && L > 0) {
+      constexpr uint32_t idS = FP8 ? tc::instr_desc(0, 0, 0, 0, 64, 128) : tc::instr_desc(1, 1, 0, 0, 64, 128);
+      constexpr uint32_t idPV = tc::instr_desc(1, 1, 0, 1, D, 128);
+      // Testing hook: bar_final gets its first arrival only from the final
+      // commit below, so this wait runs out and the CTA takes the timeout path.
+      bool ok = !P.stall || tc::mbar_wait(bar_final, 0, abort_flag, P.wait_limit);
+      ok = ok && tc::mbar_wait(bar_q, 0, abort_flag, P.wait_limit);
+      auto issue_S = [&](int m) -> bool {
+        const int s = m % kStages;
+        if (!tc::mbar_wait(bar_kfull(s), (m / kStages) & 1, abort_flag, P.wait_limit)) return false;
+        tc::fence_after_sync();
+        const uint32_t dS = tmem + ((m & 1) ? kColS1 : kColS0);
+#pragma unroll
+        for (int kk = 0; kk < C::NKS; ++kk) {
+          const int cb = kk / C::KS_PER_BLK, within = kk % C::KS_PER_BLK;
+          const uint64_t da = tc::smem_desc(sb + C::OFF_Q + cb * 128 * C::SWB + within * 32, 16, 8 * C::SWB, C::LAYOUT);
+          const uint64_t db =
+              tc::smem_desc(sb + C::OFF_K + s * C::K_BYTES + cb * 64 * C::SWB + within * 32, 16, 8 * C::SWB, C::LAYOUT);
+          if (FP8)
+            tc::mma_ss_f8(dS, da, db, idS, kk > 0 ? 1u : 0u);
+          else
+            tc::mma_ss_f16(dS, da, db, idS, kk > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(bar_sfull(m & 1));
+        return true;
+      };
+      if (ok) ok = issue_S(0);
+      if (ok && L > 1) ok = issue_S(1);
+      for (int n = 0; ok && n < L; ++n) {
+        const int s = n % kStages;
+        if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, P.wait_limit) ||
+            !tc::mbar_wait(bar_vfull(s), (n / kStages) & 1, abort_flag, P.wait_limit)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t pA = tmem + ((n & 1) ? kColS1 : kColS0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t dv = tc::smem_desc(sb + C::OFF_V + s * C::V_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
+          tc::mma_ts_f16(tmem + kColO, pA + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
+        }
+        tc::mma_commit(bar_pvdone(n & 1));
+        if (n + 2 < L && !issue_S(n + 2)) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) record_timeout(abort_flag, P.err);
+      // Every MMA issued so far has finished before TMEM is released.
+      tc::mma_commit(bar_final);
+      tc::mbar_wait(bar_final, 0, never, kWaitLimit);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- softmax
+    const int r = tid;         // query row of the block
+    const int half = r >> 6;   // 0: first chunk, 1: second
+    const bool row_exists = half == 0 || has1;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const float qsc = (FP8 && row_exists) ? P.qs[bh * g.N + (half ? i1 : i0)] : 1.f;
+    if (FP8) {
+      for (int n = tid; n < L; n += kSoftmaxThreads) uks[n] = __ldg(P.ks + bh * g.N + (ulist[n] & 0x1FFFFFu));
+      sync_softmax();
+    }
+    mod::Row row{};
+    if (row_exists) row = mod::row_of(g, M, b, half ? i1 : i0, half ? c1 : c0, colc[r & 63], r & 63);
+    const float cap = CAP ? M.cap : 1.f;
+    // Scores stay in units of `unit`: the raw products (unit = the scale, with
+    // the tile scales on the e4m3 path), or tanh values (unit = the cap); the
+    // bias is added in the same units, and one FMA per score applies
+    // c = unit log2(e). `kq` takes raw products to the argument of tanh.
+    const float slope = BIAS ? __ldg(M.slopes + head) : 0.f;
+    const float sq = P.scale * qsc, kq = sq / cap;
+    const float c_fix = (CAP ? cap : sq) * mod::kLog2e;     // c, without the key tile's scale
+    const float nslope = -slope / (CAP ? cap : sq);         // likewise
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    auto step_chunk = [&](uint32_t e) -> size_t {  // a step's chunk among all of the batch's
+      return ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.nchunk + ((e >> 21) & 0x1FFu);
+    };
+    // Rescales what this row has accumulated before step n by alpha.
+    auto rescale = [&](int n, float alpha) -> bool {
+      // O holds PV_0..PV_{n-1} once PV_{n-1} has completed.
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_pvdone((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, P.wait_limit)))
+        return false;
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int col = 0; col < D; col += 16) {
+        uint32_t o[16];
+        tc::tmem_ld16_wait(tmem + lane_base + kColO + col, o);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+        tc::tmem_st16(tmem + lane_base + kColO + col, o);
+      }
+      return true;
+    };
+    bool fresh = true;  // some row of the warp has seen no key yet
+    uint32_t e = L > 0 ? ulist[0] : 0u, ext = L > 0 ? uext[0] : 0u;
+    for (int n = 0; n < L; ++n) {
+      const bool keep = ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
+      unsigned long long vis = ~0ull;
+      bool partial = false;
+      mod::Dist dist{};
+      if (BIAS || (ext & mod::kSpecial)) {
+        const mod::Coord f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
+        if (BIAS) dist = mod::make_dist(g, M, row.at, f, FP8 && !CAP ? nslope / uks[n] : nslope);
+        if (ext & mod::kSpecial) {
+          if ((ext & mod::kHidden) && warp < 2) {
+            // V rows of hidden tokens become zeros before the product reads them.
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait(bar_vfull(n % kStages), (n / kStages) & 1, abort_flag, P.wait_limit));
+            if (ok && __ldg(M.doc_rows + 64 * step_chunk(e) + tid) < 0)
+              mod::zero_row(smem + C::OFF_V + (n % kStages) * C::V_BYTES, C::VBLK, tid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          if (keep) {
+            int vt = g.T - f.t;
+            if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
+            vis = mod::visible_box(g, &tab->col, 0, vt, g.H - f.h, g.W - f.w);
+            if (ext & mod::kDoc) vis &= mod::visible_doc(M, step_chunk(e), row.id);
+            partial = __any_sync(0xffffffffu, vis != ~0ull);
+          }
+        }
+      }
+      const float ksc = FP8 ? uks[n] : 1.f;
+      const int n1 = min(n + 1, L - 1);
+      e = ulist[n1];
+      ext = uext[n1];
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bar_sfull(n & 1), (n >> 1) & 1, abort_flag, P.wait_limit));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t sbuf = tmem + lane_base + ((n & 1) ? kColS1 : kColS0);
+      uint32_t pk[32];
+      float alpha = 1.f;
+      if (keep) {
+        const float c = FP8 && !CAP ? c_fix * ksc : c_fix, k = FP8 ? kq * ksc : kq;
+        float sum;
+        uint32_t sr[64];
+        // P and its sum from the modified scores.
+        auto exponentials = [&]() {
+          // A row that has seen no key yet has m = -inf and only -inf scores.
+          const float2 c2 = mod::bc(c), nm2 = mod::bc(m == -INFINITY ? 0.f : -m);
+          float2 ls2[4] = {mod::bc(0.f), mod::bc(0.f), mod::bc(0.f), mod::bc(0.f)};
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const float2 x = __ffma2_rn(mod::pair(sr + 2 * q), c2, nm2);
+            const float2 p = make_float2(tc::ex2(x.x), tc::ex2(x.y));
+            ls2[q & 3] = __fadd2_rn(ls2[q & 3], p);
+            pk[q] = mod::pack(p);
+          }
+          const float2 ls = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
+          sum = ls.x + ls.y;
+        };
+        // Once more with the row maxima when a score turns out to be far above
+        // its row's reference.
+        bool done = false;
+        for (bool measure = fresh; !done; measure = true) {
+          tc::tmem_ld64_wait(sbuf, sr);
+          if (CAP) {
+            if (partial) mod::set_unseen<64>(sr, vis, 0.f);
+            mod::tanh_scores<64>(sr, k);
+          }
+          if (BIAS) mod::add_distance<64>(g, reinterpret_cast<float*>(sr), &tab->col, 0, dist);
+          if (partial) mod::set_unseen<64>(sr, vis, -INFINITY);
+          if (measure) {
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              mx4[q & 3] = tc::fmax3(mx4[q & 3], __uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1]));
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+            if (mx > m + kRaise) {  // m = -inf: the row has seen no key and its O row is zero
+              if (m != -INFINITY) alpha = tc::ex2(m - (mx + kAbove));
+              m = mx + kAbove;
+            }
+            fresh = __any_sync(0xffffffffu, m == -INFINITY);
+          }
+          exponentials();
+          done = measure || __all_sync(0xffffffffu, sum <= kSumLimit);
+        }
+        l = l * alpha + sum;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) pk[q] = 0u;
+      }
+      tc::tmem_st32(sbuf, pk);  // P_n over the first 32 columns of S_n
+      if (__any_sync(0xffffffffu, alpha != 1.f) && !rescale(n, alpha)) {
+        ok = false;
+        break;
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar_pfull(n & 1));
+    }
+    if (!ok) record_timeout(abort_flag, P.err);
+    // ---------------------------------------------------------- epilogue
+    if (ok && L > 0) {
+      if (!__all_sync(0xffffffffu,
+                      tc::mbar_wait(bar_pvdone((L - 1) & 1), ((L - 1) >> 1) & 1, abort_flag, P.wait_limit))) {
+        record_timeout(abort_flag, P.err);
+        ok = false;
+      }
+      tc::fence_after_sync();
+    }
+    int* tokrow = reinterpret_cast<int*>(smem + C::OFF_TOK);
+    if (NAT) {
+      const bool real = row_exists && (r & 63) < g.cr && row.at.t < g.T && row.at.h < g.H && row.at.w < g.W;
+      tokrow[r] = real ? (row.at.t * g.H + row.at.h) * g.W + row.at.w : -1;
+    }
+    if (!row.live) l = 0.f;  // padded or hidden: a zero row
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
+#pragma unroll
+    for (int col = 0; col < D; col += 32) {
+      uint32_t o[32];
+      if (ok && L > 0) {
+        tc::tmem_ld32_wait(tmem + lane_base + kColO + col, o);
+      }
+      if (!(ok && L > 0 && row.live)) {  // whatever the row holds, NaN included
+#pragma unroll
+        for (int q = 0; q < 32; ++q) o[q] = 0u;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) w[q] = mod::pack(__fmul2_rn(mod::pair(o + 2 * q), mod::bc(inv)));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+    if (P.lse && row_exists) {
+      const float lse_r = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (NAT) {
+        if (tokrow[r] >= 0) P.lse[bh * (size_t)g.L + (size_t)tokrow[r]] = lse_r;
+      } else {
+        P.lse[(size_t)tiled_row(half ? i1 : i0, half ? c1 : c0) + (r & 63)] = lse_r;
+      }
+    }
+    sync_softmax();
+    constexpr int CPR = D / 8;  // 16-byte pieces per row
+    const int rows = has1 ? 128 : 64;
+    for (int e2 = tid; e2 < rows * CPR; e2 += kSoftmaxThreads) {
+      const int rr = e2 / CPR, cc = e2 % CPR;
+      const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_K + rr * C::O_PITCH + cc * 16);
+      if (NAT) {
+        const int n = tokrow[rr];
+        if (n >= 0) reinterpret_cast<uint4*>(P.o + (((size_t)b * g.L + n) * g.Hh + head) * D)[cc] = val;
+      } else {
+        uint4* og = reinterpret_cast<uint4*>(P.o + (size_t)tiled_row(rr >> 6 ? i1 : i0, rr >> 6 ? c1 : c0) * D);
+        og[(rr & 63) * CPR + cc] = val;
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool FP8, bool NAT, bool CAP, bool BIAS>
+bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v, const Params& prm,
+                  cudaStream_t st) {
+  using C = Cfg<D, FP8>;
+  const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
+  if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  CUtensorMap mq, mk, mv;
+  const CUtensorMapDataType dqk = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = C::SWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (NAT && !FP8 ? !bsattn_make_map_nat(&mq, q, p) || !bsattn_make_map_nat(&mk, k, p)
+                  : !bsattn_make_map_2d(&mq, q, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw) ||
+                        !bsattn_make_map_2d(&mk, k, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw))
+    return BSATTN_ERR_CUDA;
+  if (NAT ? !bsattn_make_map_nat(&mv, v, p)
+          : !bsattn_make_map_2d(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return BSATTN_ERR_CUDA;
+  size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * (FP8 ? 12 : 8);
+  if (smem < 80 * 1024) smem = 80 * 1024;  // at most two CTAs (2 x 256 TMEM columns) per SM
+  if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
+  auto kern = attn_mod_tc_kernel<D, FP8, NAT, CAP, BIAS>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return BSATTN_ERR_CUDA;
+  dim3 grid(attention_items(p), p->desc.heads, p->desc.B);
+  kern<<<grid, kThreads, smem, st>>>(mq, mk, mv, prm);
+  return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+template <int D, bool FP8, bool NAT>
+bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v, const Params& prm,
+                  cudaStream_t st) {
+  if (prm.mod.cap > 0.f)
+    return prm.mod.slopes ? run<D, FP8, NAT, true, true>(p, q, k, v, prm, st)
+                          : run<D, FP8, NAT, true, false>(p, q, k, v, prm, st);
+  return prm.mod.slopes ? run<D, FP8, NAT, false, true>(p, q, k, v, prm, st)
+                        : run<D, FP8, NAT, false, false>(p, q, k, v, prm, st);
+}
+
+}  // namespace
+
+bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
+                                   const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
+                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, cudaStream_t st, AttnLayout lay) {
+  if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
+  Params prm;
+  prm.g = make_geom(p);
+  prm.mod = mod;
+  prm.qs = qs;
+  prm.ks = ks;
+  prm.idx = idx;
+  prm.cnt = cnt;
+  prm.kmax = p->kmax;
+  prm.o = o;
+  prm.lse = lse;
+  prm.scale = p->scale;
+  prm.err = p->d_err;
+  // The union of two lists of one-chunk tiles, or one list of tiles times their chunks.
+  prm.umax = p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax)
+                            : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+  prm.bm_words = (p->N + 31) / 32;
+  prm.pair_axis = pair_axis_of(p);
+  prm.stall = bsattn_testing_timeout_forced() ? 1 : 0;
+  prm.wait_limit = prm.stall ? kTestWaitLimit : kWaitLimit;
+  const int nd[3] = {p->nT, p->nH, p->nW};
+  for (int a = 0; a < 3; ++a) prm.pdim[a] = a == prm.pair_axis ? (nd[a] + 1) / 2 : nd[a];
+  const bool fp8 = p->desc.qk_fp8 != 0, d128 = p->desc.head_dim == 128;
+  if (lay == AttnLayout::Natural)
+    return d128 ? (fp8 ? run<128, true, true>(p, q, k, v, prm, st) : run<128, false, true>(p, q, k, v, prm, st))
+                : (fp8 ? run<64, true, true>(p, q, k, v, prm, st) : run<64, false, true>(p, q, k, v, prm, st));
+  return d128 ? (fp8 ? run<128, true, false>(p, q, k, v, prm, st) : run<128, false, false>(p, q, k, v, prm, st))
+              : (fp8 ? run<64, true, false>(p, q, k, v, prm, st) : run<64, false, false>(p, q, k, v, prm, st));
+}

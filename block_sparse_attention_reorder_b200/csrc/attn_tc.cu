@@ -34,10 +34,8 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include <type_traits>
 
 #include "internal.h"
-#include "score_mod.cuh"
 #include "tc_common.cuh"
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no
@@ -64,6 +62,24 @@ bool bsattn_make_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType 
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Natural-layout tensor [B, T, H, W, Hh * D] as five dimensions, innermost
+// first, with a one-chunk box of 64 columns (128 bytes, one swizzle span).
+bool bsattn_make_map_nat(CUtensorMap* map, const void* base, const bsattn_plan* p) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bsattn_desc& d = p->desc;
+  const cuuint64_t row = (cuuint64_t)d.heads * d.head_dim * 2;  // bytes per token
+  cuuint64_t dims[5] = {(cuuint64_t)d.heads * d.head_dim, (cuuint64_t)d.W, (cuuint64_t)d.H, (cuuint64_t)d.T,
+                        (cuuint64_t)d.B};
+  cuuint64_t strides[4] = {row, row * d.W, row * d.W * d.H, row * d.W * d.H * d.T};
+  cuuint32_t box[5] = {64, (cuuint32_t)p->cw, (cuuint32_t)p->ch, (cuuint32_t)p->ct, 1};  // one chunk
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -98,12 +114,7 @@ struct TcParams {
   int stall;             // testing: the MMA thread first waits on a barrier nothing arrives at
 };
 
-struct TcParamsMod : TcParams {
-  ModParams mod;
-  float scale;
-};
-
-template <int D, bool FP8, bool MOD>
+template <int D, bool FP8>
 struct Cfg {
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int QRB = D * ESZ;                 // Q/K row bytes
@@ -126,9 +137,7 @@ struct Cfg {
   static constexpr int OFF_COL = OFF_MISC + 16;         // 64 packed column coords
   static constexpr int OFF_SCAN = OFF_COL + 256;        // block-scan scratch
   static constexpr int OFF_TOK = OFF_SCAN + 64;         // epilogue: natural token of each block row
-  static constexpr int OFF_TAB = OFF_TOK + 512;         // score rules: a chunk's row offsets
-  static constexpr int OFF_DYN = OFF_TAB + (MOD ? (int)sizeof(mod::Table) : 0);  // bitmaps, union list
-  static_assert(OFF_TAB % 16 == 0, "float4 reads of the table");
+  static constexpr int OFF_DYN = OFF_TOK + 512;         // bitmaps, union list
   static constexpr int O_PITCH = D * 2 + 16;            // epilogue staging row pitch
   static_assert(OFF_Q % 1024 == 0 && OFF_K % 1024 == 0 && OFF_V % 1024 == 0, "alignment");
   static_assert(128 * O_PITCH <= OFF_BAR - OFF_K, "epilogue staging fits in the ring");
@@ -150,16 +159,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi, float& sum) 
 // layout [B, L, Hh, D] directly (else all tiled). Natural reads go
 // through five-dimensional tensor maps whose box is one tile. e4m3 Q/K are
 // always tile codes (tiled layout).
-// MOD: score rules (score_mod.cuh) on the scores between the S product and
-// the softmax. The step list is filtered by them at set-up, so that chunks
-// hidden from the whole block cost nothing; of the rest only steps that need
-// element masks evaluate them. uext then holds packed coordinates and flags.
-template <int D, bool FP8, bool NAT, bool MOD>
+template <int D, bool FP8, bool NAT>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ std::conditional_t<MOD, TcParamsMod, TcParams> P) {
-  using C = Cfg<D, FP8, MOD>;
+               const __grid_constant__ CUtensorMap tmV, TcParams P) {
+  using C = Cfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -180,7 +184,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   volatile int* never = reinterpret_cast<volatile int*>(misc + 3);  // stays 0: waits that ignore abort
   uint32_t* colc = reinterpret_cast<uint32_t*>(smem + C::OFF_COL);
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
-  mod::Table* coltab = reinterpret_cast<mod::Table*>(smem + C::OFF_TAB);  // score rules only
   uint32_t* bmA = reinterpret_cast<uint32_t*>(smem + C::OFF_DYN);
   uint32_t* bmB = bmA + P.bm_words;
   uint32_t* ulist = bmB + P.bm_words;
@@ -303,10 +306,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     tc::tmem_relinquish();
   }
   if (tid < 64) colc[tid] = chunk_row_code(g, tid);  // in-chunk (t, h, w) offsets of each chunk row
-  int prefix = 0;
-  if constexpr (MOD) {
-    if (P.mod.prefix) prefix = __ldg(P.mod.prefix + b);
-  }
   if (g.cr < 64) {
     // Tiles of fewer than 64 tokens: natural-layout loads fill only the
     // chunk box's rows; the rest of every V slot must hold finite values.
@@ -409,15 +408,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
     }
     if (tid == 0) misc[2] = (uint32_t)min(tot, P.umax);
-  }
-  if constexpr (MOD) {
-    mod::fill_table<kThreads>(g, coltab, colc);
-    __syncthreads();
-    const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext,
-                                                        nchunk > 1 ? uorg : nullptr, steps, scan);
-    __syncthreads();
-    if (tid == 0) misc[2] = (uint32_t)left;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -570,7 +560,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const bool row_exists = half == 0 || has1;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const float qsc = (FP8 && row_exists) ? P.qs[bh * g.N + (half ? i1 : i0)] : 1.f;
-    if ((nchunk == 1 && !MOD) || FP8) {
+    if (nchunk == 1 || FP8) {
       // Extents of one-chunk tiles, spread over the softmax threads (the
       // compaction above leaves them out: a dense bitmap word would put up
       // to 32 entries' divisions on one thread ahead of the CTA barrier),
@@ -578,19 +568,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // at once rather than one global load per step on the critical path.
       for (int n = r; n < L; n += 128) {
         const int jn = (int)(ulist[n] & 0x1FFFFFu);
-        if (nchunk == 1 && !MOD) uext[n] = chunk_ext(jn, ChunkOrigin{0, 0, 0});
+        if (nchunk == 1) uext[n] = chunk_ext(jn, ChunkOrigin{0, 0, 0});
         if (FP8) uks[n] = __ldg(P.ks + bh * g.N + jn);
       }
       asm volatile("bar.sync 2, 128;" ::: "memory");
     }
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    mod::Row row{};
-    float slope = 0.f;
-    if constexpr (MOD) {
-      if (row_exists) row = mod::row_of(g, P.mod, b, half ? i1 : i0, half ? c1 : c0, colc[r & 63], r & 63);
-      if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
-    }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
       const bool keep = ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
@@ -603,57 +587,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       uint32_t pk[32];
       bool need = false;
       float alpha = 1.f;
-      if constexpr (MOD) {
-        if ((uext[n] & mod::kHidden) && warp < 2) {
-          // V rows of hidden tokens become zeros before the product reads them.
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_vfull(n % kStages), (n / kStages) & 1, abort_flag, P.wait_limit))) {
-            ok = false;
-            break;
-          }
-          const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
-          if (__ldg(P.mod.doc_rows + first + r) < 0) mod::zero_row(smem + C::OFF_V + (n % kStages) * C::V_BYTES, C::VBLK, r);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-      }
       if (keep) {
         uint32_t sr[64];
         tc::tmem_ld64_wait(sbuf, sr);
-        float c = P.scale_log2 * (FP8 ? qsc * uks[n] : 1.f);
+        const float c = P.scale_log2 * (FP8 ? qsc * uks[n] : 1.f);
         const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
-        if constexpr (MOD) {
-          // Scores stay in units of `unit`: the raw products (unit = the
-          // scale), or tanh values (unit = the cap); the bias is added in the
-          // same units, and one FMA per score applies c = unit log2(e) as
-          // without rules.
-          const ModParams& M = P.mod;
-          float unit = P.scale * (FP8 ? qsc * uks[n] : 1.f);
-          if (M.cap > 0.f) {
-            mod::tanh_scores<64>(sr, unit / M.cap);
-            unit = M.cap;
-          }
-          c = unit * mod::kLog2e;
-          const mod::Coord f = mod::chunk_first(g, M, ext, step_origin(n));
-          if (M.slopes) {
-            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
-            const float per = -slope / unit;
-            const float nw[3] = {per * M.dist[0], per * M.dist[1], per * M.dist[2]};
-            mod::add_distance<64>(g, reinterpret_cast<float*>(sr), coltab, 0, at, nw);
-          }
-          if (ext & (mod::kEdge | mod::kCausal | mod::kDoc)) {
-            int vt = g.T - f.t;
-            if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
-            unsigned long long vis = mod::visible_box(g, coltab, 0, vt, g.H - f.h, g.W - f.w);
-            if (ext & mod::kDoc)
-              vis &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * nchunk + ((e >> 21) & 0x1FFu), row.id);
-            if (__any_sync(0xffffffffu, vis != ~0ull)) {
-              const uint32_t v2[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
-#pragma unroll
-              for (int q = 0; q < 64; ++q)
-                if (!((v2[q / 32] >> (q % 32)) & 1u)) sr[q] = 0xff800000u;  // -inf
-            }
-          }
-        } else if (edge) {  // padded keys of an edge chunk
+        if (edge) {  // padded keys of an edge chunk
           const int vt = (int)(ext & 0xffu), vh = (int)((ext >> 8) & 0xffu), vw = (int)((ext >> 16) & 0xffu);
 #pragma unroll
           for (int q = 0; q < 64; ++q) {
@@ -671,7 +611,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         const float m_new = fmaxf(m, mx);
         if (m == -INFINITY) {
-          m = m_new;  // first kept tile of this row (with rules: that shows it a key): O row is still zero
+          m = m_new;  // first kept tile of this row: O row is still zero
         } else if (m_new - m > kRescaleThreshold) {
           alpha = tc::ex2(m - m_new);
           m = m_new;
@@ -683,9 +623,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // CTAs' softmax warps, is not the bottleneck; edge tiles (with -inf
         // for padded keys) use the SFU throughout. The row sum uses the fp32
         // values, four packed chains.
-        // A row that has seen no key yet has m = -inf and only -inf scores.
-        const float ms = MOD && m == -INFINITY ? 0.f : m;
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(-ms, -ms);
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-m, -m);
         float2 ls2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
         auto emit = [&](int q, float2 pv) {
@@ -693,7 +631,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           __nv_bfloat162 hv = __floats2bfloat162_rn(pv.x, pv.y);
           pk[q] = *reinterpret_cast<uint32_t*>(&hv);
         };
-        if (MOD || edge) {
+        if (edge) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1])), c2, nm2);
@@ -744,9 +682,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       tc::fence_after_sync();
     }
-    if constexpr (MOD) {
-      if (!row.live) l = 0.f;  // padded or hidden: a zero row
-    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
 #pragma unroll
@@ -757,12 +692,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       } else {
 #pragma unroll
         for (int q = 0; q < 32; ++q) o[q] = 0u;
-      }
-      if constexpr (MOD) {
-        if (!row.live) {  // whatever the row holds, NaN included
-#pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = 0u;
-        }
       }
       uint32_t w[16];
       float dummy = 0.f;
@@ -824,38 +753,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host side
-// Natural-layout tensor [B, T, H, W, Hh * D] as five dimensions, innermost
-// first, with a one-chunk box of 64 columns (128 bytes, one swizzle span).
-bool make_map_nat(CUtensorMap* map, const void* base, const bsattn_plan* p) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const bsattn_desc& d = p->desc;
-  const cuuint64_t row = (cuuint64_t)d.heads * d.head_dim * 2;  // bytes per token
-  cuuint64_t dims[5] = {(cuuint64_t)d.heads * d.head_dim, (cuuint64_t)d.W, (cuuint64_t)d.H, (cuuint64_t)d.T,
-                        (cuuint64_t)d.B};
-  cuuint64_t strides[4] = {row, row * d.W, row * d.W * d.H, row * d.W * d.H * d.T};
-  cuuint32_t box[5] = {64, (cuuint32_t)p->cw, (cuuint32_t)p->ch, (cuuint32_t)p->ct, 1};  // one chunk
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-template <int D, bool FP8, bool NAT, bool MOD>
+template <int D, bool FP8, bool NAT>
 bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v,
-                  const std::conditional_t<MOD, TcParamsMod, TcParams>& prm, cudaStream_t st) {
-  using C = Cfg<D, FP8, MOD>;
+                  TcParams prm, cudaStream_t st) {
+  using C = Cfg<D, FP8>;
   const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
   if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
   const CUtensorMapDataType dqk = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = C::SWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (NAT && !FP8 ? !make_map_nat(&mq, q, p) : !bsattn_make_map_2d(&mq, q, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw))
+  if (NAT && !FP8 ? !bsattn_make_map_nat(&mq, q, p) : !bsattn_make_map_2d(&mq, q, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw))
     return BSATTN_ERR_CUDA;
-  if (NAT && !FP8 ? !make_map_nat(&mk, k, p) : !bsattn_make_map_2d(&mk, k, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw))
+  if (NAT && !FP8 ? !bsattn_make_map_nat(&mk, k, p) : !bsattn_make_map_2d(&mk, k, dqk, C::ESZ, D, rows, C::SWB / C::ESZ, 64, sw))
     return BSATTN_ERR_CUDA;
-  if (NAT ? !make_map_nat(&mv, v, p)
+  if (NAT ? !bsattn_make_map_nat(&mv, v, p)
           : !bsattn_make_map_2d(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return BSATTN_ERR_CUDA;
   // Step list, extents and (tiles of several chunks) chunk offsets.
@@ -863,7 +774,7 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
                 (FP8 ? (size_t)prm.umax * 4 : 0);
   if (smem < 80 * 1024) smem = 80 * 1024;  // at most two CTAs (2 x 256 TMEM columns) per SM
   if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
-  auto kern = attn_tc_kernel<D, FP8, NAT, MOD>;
+  auto kern = attn_tc_kernel<D, FP8, NAT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
   const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
@@ -879,9 +790,9 @@ size_t attention_workspace_bytes(const bsattn_plan*) { return 0; }
 bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* k, const float* qs,
                                const float* ks, const __nv_bfloat16* v, const int32_t* idx,
                                const int32_t* cnt, __nv_bfloat16* o, float* lse, void*, size_t,
-                               cudaStream_t st, AttnLayout lay, const ModParams* mod) {
+                               cudaStream_t st, AttnLayout lay) {
   if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
-  TcParamsMod prm;
+  TcParams prm;
   prm.g = make_geom(p);
   prm.qs = qs;
   prm.ks = ks;
@@ -903,18 +814,10 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
   const int nd[3] = {p->nT, p->nH, p->nW};
   for (int a = 0; a < 3; ++a) prm.pdim[a] = a == prm.pair_axis ? (nd[a] + 1) / 2 : nd[a];
   const bool fp8 = p->desc.qk_fp8 != 0, d128 = p->desc.head_dim == 128;
-  if (mod) {
-    prm.mod = *mod;
-    prm.scale = p->scale;
-  }
-#define BSATTN_RUN(NATV, MODV)                                                                                        \
-  return d128 ? (fp8 ? run<128, true, NATV, MODV>(p, q, k, v, prm, st) : run<128, false, NATV, MODV>(p, q, k, v, prm, st)) \
-              : (fp8 ? run<64, true, NATV, MODV>(p, q, k, v, prm, st) : run<64, false, NATV, MODV>(p, q, k, v, prm, st))
-  if (mod) {
-    if (lay == AttnLayout::Natural) BSATTN_RUN(true, true);
-    BSATTN_RUN(false, true);
-  }
-  if (lay == AttnLayout::Natural) BSATTN_RUN(true, false);
-  BSATTN_RUN(false, false);
+#define BSATTN_RUN(NATV)                                                                            \
+  return d128 ? (fp8 ? run<128, true, NATV>(p, q, k, v, prm, st) : run<128, false, NATV>(p, q, k, v, prm, st)) \
+              : (fp8 ? run<64, true, NATV>(p, q, k, v, prm, st) : run<64, false, NATV>(p, q, k, v, prm, st))
+  if (lay == AttnLayout::Natural) BSATTN_RUN(true);
+  BSATTN_RUN(false);
 #undef BSATTN_RUN
 }

@@ -52,6 +52,7 @@
 
 #include "internal.h"
 #include "score_mod.cuh"
+#include "steps.cuh"
 #include "tc_common.cuh"
 
 namespace {
@@ -61,25 +62,6 @@ constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColG = 384;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
-
-// Score rules: a chunk's row offsets, and every chunk's in-tile origin
-// (packed 10 bits per axis), so that a step needs no division.
-struct ModTab {
-  mod::Table col;
-  uint32_t origin[kMaxChunks];
-  __device__ __forceinline__ ChunkOrigin at(int c) const {
-    const uint32_t v = origin[c];
-    return ChunkOrigin{(int)(v & 0x3FFu), (int)((v >> 10) & 0x3FFu), (int)(v >> 20)};
-  }
-};
-template <int NT>
-__device__ __forceinline__ void fill_modtab(const Geom& g, ModTab* tab, const uint32_t* colc) {
-  mod::fill_table<NT>(g, &tab->col, colc);
-  for (int c = threadIdx.x; c < g.nchunk; c += NT) {
-    const ChunkOrigin o = chunk_origin(g, c);
-    tab->origin[c] = (uint32_t)o.dt | ((uint32_t)o.dh << 10) | ((uint32_t)o.dw << 20);
-  }
-}
 
 struct DqParams {
   Geom g;
@@ -128,106 +110,6 @@ struct DqCfg {
   static constexpr int O_PITCH = D * 2 + 16;           // epilogue staging pitch
   static_assert(128 * O_PITCH <= OFF_BAR - OFF_K, "epilogue staging fits in the rings");
 };
-
-// Work item -> its two (tile, chunk) halves; i1 = -1 when the second half is
-// absent. 64-token tiles: adjacent tiles along the pair axis. Tiles of several
-// chunks: chunks 2b and 2b + 1 of one tile (padding-only chunks included, so
-// that their rows of the tiled gradients are written, as zeros).
-__device__ __forceinline__ void block_halves(const Geom& g, int pair_axis, const int* pdim, int item, int* i0,
-                                             int* i1, int* c0, int* c1) {
-  if (g.nchunk > 1) {
-    const int per = (g.nchunk + 1) / 2;
-    *i0 = *i1 = item / per;
-    *c0 = 2 * (item % per);
-    *c1 = *c0 + 1;
-    if (*c1 >= g.nchunk) *i1 = -1;
-    return;
-  }
-  const int nd[3] = {g.nT, g.nH, g.nW};
-  int c[3], rem = item;
-  c[2] = rem % pdim[2];
-  rem /= pdim[2];
-  c[1] = rem % pdim[1];
-  c[0] = rem / pdim[1];
-  c[pair_axis] *= 2;
-  *i0 = (c[0] * g.nH + c[1]) * g.nW + c[2];
-  c[pair_axis] += 1;
-  *i1 = c[pair_axis] < nd[pair_axis] ? (c[0] * g.nH + c[1]) * g.nW + c[2] : -1;
-  *c0 = *c1 = 0;
-}
-
-// Whether chunk c of tile j holds a real token (its first row is in the grid).
-__device__ __forceinline__ bool chunk_is_real(const Geom& g, int j, int c) {
-  const ChunkOrigin o = chunk_origin(g, c);
-  const int bt = j / (g.nH * g.nW), bhh = (j / g.nW) % g.nH, bw = j % g.nW;
-  return bt * g.tt + o.dt < g.T && bhh * g.th + o.dh < g.H && bw * g.tw + o.dw < g.W;
-}
-
-// Compacts the union of two tile bitmaps into the ascending step list, one
-// step per real 64-row chunk of each listed tile: tile in bits 0-20, chunk in
-// bits 21-29, bit 30 (31) from the first (second) bitmap; ext gets the
-// chunk's real extent from its first token (t, h, w bytes, capped at 255) and
-// bit 31 when the chunk has padded rows. *count = steps (capped at cap). All
-// threads of the CTA take part; the block-scan scratch holds one int per warp.
-template <int NT>
-__device__ __forceinline__ void compact_steps(const Geom& g, const uint32_t* bmA, const uint32_t* bmB, int words,
-                                              uint32_t* list, uint32_t* ext, int cap, int* scan, uint32_t* count) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wpt = (words + NT - 1) / NT;
-  const int w0 = min(tid * wpt, words), w1 = min(w0 + wpt, words);
-  int mine = 0;
-  for (int w = w0; w < w1; ++w) {
-    uint32_t bits = bmA[w] | bmB[w];
-    if (g.nchunk == 1) {
-      mine += __popc(bits);
-    } else {
-      while (bits) {
-        const int j = w * 32 + __ffs(bits) - 1;
-        for (int c = 0; c < g.nchunk; ++c) mine += chunk_is_real(g, j, c) ? 1 : 0;
-        bits &= bits - 1;
-      }
-    }
-  }
-  int x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) scan[warp] = x;
-  __syncthreads();
-  int off = 0, tot = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) {
-    off += i < warp ? scan[i] : 0;
-    tot += scan[i];
-  }
-  int pos = off + x - mine;
-  for (int w = w0; w < w1; ++w) {
-    const uint32_t a = bmA[w], bb = bmB[w];
-    uint32_t bits = a | bb;
-    while (bits) {
-      const int bit = __ffs(bits) - 1;
-      bits &= bits - 1;
-      const int j = w * 32 + bit;
-      const uint32_t e = (uint32_t)j | (((a >> bit) & 1u) << 30) | (((bb >> bit) & 1u) << 31);
-      const int bt = j / (g.nH * g.nW), bhh = (j / g.nW) % g.nH, bw = j % g.nW;
-      for (int c = 0; c < g.nchunk; ++c) {
-        if (g.nchunk > 1 && !chunk_is_real(g, j, c)) continue;
-        if (pos < cap) {
-          const ChunkOrigin o = chunk_origin(g, c);
-          const int vt = min(g.T - bt * g.tt - o.dt, 255), vh = min(g.H - bhh * g.th - o.dh, 255),
-                    vw = min(g.W - bw * g.tw - o.dw, 255);
-          const bool edge = vt < g.ct || vh < g.ch || vw < g.cw || g.cr < 64;
-          list[pos] = e | ((uint32_t)c << 21);
-          ext[pos] = (uint32_t)vt | ((uint32_t)vh << 8) | ((uint32_t)vw << 16) | (edge ? 1u << 31 : 0u);
-        }
-        ++pos;
-      }
-    }
-  }
-  if (tid == 0) *count = (uint32_t)min(tot, cap);
-}
 
 template <int D, bool MOD, int kStages>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -332,7 +214,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, nullptr, steps, scan);
+    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
     __syncthreads();
     if (tid == 0) misc[2] = (uint32_t)left;
   }
@@ -452,6 +334,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const float c = P.scale_log2;
     bool ok = true;
     mod::Row row{};
+    float kc = 0.f;  // takes raw scores to the argument of tanh
     float slope = 0.f;
     float2 sw2 = mod::bc(0.f), swd2 = sw2, spd2 = sw2;  // sums of w = P (dP - Delta), w dist, P dist
     float nlse2 = -lse2, ndlt = -dlt;
@@ -462,6 +345,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ndlt = 0.f;
       }
       if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
+      if (P.mod.cap > 0.f) kc = P.scale / P.mod.cap;
     }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
@@ -503,15 +387,15 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // log2 of P = raw scores (or tanh values) times c2, bias, minus the log-sum-exp.
           float c2 = c;
           if (M.cap > 0.f) {
-            mod::tanh_scores<32>(sr, P.scale / M.cap);
             c2 = M.cap * mod::kLog2e;
+            if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) mod::set_unseen<32>(sr, vis, 0.f);
+            mod::tanh_scores<32>(sr, kc);
           }
           float far[32];
           if (M.slopes) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) far[q] = 0.f;
-            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
-            mod::add_distance<32>(g, far, &tab->col, 32 * part, at, M.dist);
+            mod::add_distance<32>(g, far, &tab->col, 32 * part, mod::make_dist(g, M, row.at, f, 1.f));
           }
           const float2 cc2 = mod::bc(c2), ss2 = mod::bc(-slope * mod::kLog2e), nl2 = mod::bc(nlse2), nd2 = mod::bc(ndlt);
           auto form = [&](auto masked, auto cap, auto bias) {
@@ -866,7 +750,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, nullptr, steps, scan);
+    const int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, steps, scan);
     __syncthreads();
     if (tid == 0) misc[2] = (uint32_t)left;
   }
@@ -990,10 +874,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const float c = P.scale_log2;
     bool ok = true;
     mod::Row row{};
+    float kc = 0.f;  // takes raw scores to the argument of tanh
     float slope = 0.f;
     if constexpr (MOD) {
       if (row_exists) row = mod::row_of(g, P.mod, b, half ? j1 : j0, half ? kc1 : kc0, colc[r & 63], r & 63);
       if (P.mod.slopes) slope = __ldg(P.mod.slopes + head);
+      if (P.mod.cap > 0.f) kc = P.scale / P.mod.cap;
     }
     for (int n = 0; n < L; ++n) {
       const uint32_t e = ulist[n];
@@ -1043,17 +929,15 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
           float c2 = c;
           if (M.cap > 0.f) {
-            mod::tanh_scores<32>(sr, P.scale / M.cap);
             c2 = M.cap * mod::kLog2e;
+            if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) mod::set_unseen<32>(sr, vis, 0.f);
+            mod::tanh_scores<32>(sr, kc);
           }
           float y[32];  // -lse log2(e) of the queries, plus the bias
 #pragma unroll
           for (int q = 0; q < 8; ++q) *reinterpret_cast<float4*>(y + 4 * q) = reinterpret_cast<const float4*>(ld + 32 * part)[q];
           if (M.slopes) {
-            const float at[3] = {(float)(row.at.t - f.t), (float)(row.at.h - f.h), (float)(row.at.w - f.w)};
-            const float s2 = -slope * mod::kLog2e;
-            const float nw[3] = {s2 * M.dist[0], s2 * M.dist[1], s2 * M.dist[2]};
-            mod::add_distance<32>(g, y, &tab->col, 32 * part, at, nw);
+            mod::add_distance<32>(g, y, &tab->col, 32 * part, mod::make_dist(g, M, row.at, f, -slope * mod::kLog2e));
           }
           const float2 cc2 = mod::bc(c2);
           auto form = [&](auto masked, auto cap, auto) {

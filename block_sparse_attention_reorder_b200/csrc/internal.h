@@ -183,7 +183,11 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
                                const float* qs, const float* ks, const __nv_bfloat16* v,
                                const int32_t* idx, const int32_t* cnt, __nv_bfloat16* o,
                                float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
-                               AttnLayout lay, const ModParams* mod = nullptr);
+                               AttnLayout lay);
+// The same under score rules (csrc/attn_mod_tc.cu).
+bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
+                                   const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
+                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, cudaStream_t st, AttnLayout lay);
 // Tile axis (0 = t, 1 = h, 2 = w) along which two 64-token tiles are stacked
 // into one 128-row block (attention: query tiles; dK/dV: key tiles). Top-k and
 // top-p: t, whose neighbouring tiles keep the most key tiles in common on the
@@ -239,6 +243,8 @@ bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv
                           const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1, bool transpose,
                           const int32_t* doc, cudaStream_t st);
 
+// Natural-layout tensor map [B, T, H, W, heads * D] whose box is one chunk.
+bool bsattn_make_map_nat(CUtensorMap* map, const void* base, const bsattn_plan* p);
 // 2-D tiled tensor map over `rows` rows of `inner` elements of `esz` bytes.
 bool bsattn_make_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esz, int inner,
                         uint64_t rows, int box_inner, int box_rows, CUtensorMapSwizzle sw);

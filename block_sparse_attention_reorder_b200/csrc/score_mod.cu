@@ -325,8 +325,8 @@ bsattn_status forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const
   if (dev.status) return dev.status;
   if ((s = launch_doc_prep(p, m, w, (cudaStream_t)stream))) return s;
   const ModParams d = device_mod(p, m, w);
-  return launch_attention(p, q, k, qs, ks, (const __nv_bfloat16*)v, idx, cnt, (__nv_bfloat16*)o, lse, nullptr, 0,
-                          (cudaStream_t)stream, lay, &d);
+  return launch_attention_mod(p, d, q, k, qs, ks, (const __nv_bfloat16*)v, idx, cnt, (__nv_bfloat16*)o, lse,
+                              (cudaStream_t)stream, lay);
 }
 
 }  // namespace
@@ -449,8 +449,11 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
     qa = w.qc;
     ka = w.kc;
   }
+  if (m)
+    return launch_attention_mod(p, d, qa, ka, w.qs, w.ks, (const __nv_bfloat16*)v_nat, idx, cnt, (__nv_bfloat16*)o_nat,
+                                lse_nat, st, AttnLayout::Natural);
   return launch_attention(p, qa, ka, w.qs, w.ks, (const __nv_bfloat16*)v_nat, idx, cnt, (__nv_bfloat16*)o_nat, lse_nat,
-                          nullptr, 0, st, AttnLayout::Natural, m ? &d : nullptr);
+                          nullptr, 0, st, AttnLayout::Natural);
 }
 
 }  // extern "C"

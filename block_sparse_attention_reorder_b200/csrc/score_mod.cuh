@@ -66,41 +66,48 @@ __device__ __forceinline__ float tanh_any(float u) {
   return fmaf(-2.f, rcp(tc::ex2(u * (2.f * kLog2e)) + 1.f), 1.f);
 }
 
-// Replaces raw scores s[] by tanh(k s) (k = scale / cap). The polynomials
-// serve a whole warp's values when the largest is small, which usual scores
-// under a usual cap are; else the SFU form does, and the polynomial where |u|
-// is small. The forms agree to about 2e-7 of the value.
+// Replaces raw scores s[] by tanh(k s) (k = scale / cap) in the form that TIER
+// names: 0 and 1 the polynomials, 2 the polynomial where |u| is small (most
+// values even under a low cap: the branch is seldom taken) and else the SFU
+// form. The forms agree to about 2e-7 of the value.
+template <int TIER, int N>
+__device__ __forceinline__ void tanh_form(uint32_t* s, float k) {
+  const float2 k2 = bc(k);
+#pragma unroll
+  for (int q = 0; q < N; q += 2) {
+    const float2 u = __fmul2_rn(pair(s + q), k2), t = TIER == 0 ? tanh_tiny2(u) : tanh_small2(u);
+    s[q] = __float_as_uint(TIER < 2 || fabsf(u.x) <= kSmall ? t.x : tanh_any(u.x));
+    s[q + 1] = __float_as_uint(TIER < 2 || fabsf(u.y) <= kSmall ? t.y : tanh_any(u.y));
+  }
+}
+// Greatest |s|; a NaN is passed over.
 template <int N>
-__device__ __forceinline__ void tanh_scores(uint32_t* s, float k) {
+__device__ __forceinline__ float greatest(const uint32_t* s) {
   float mx4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int q = 0; q < N; q += 2)
     mx4[(q / 2) & 3] = tc::fmax3(mx4[(q / 2) & 3], fabsf(__uint_as_float(s[q])), fabsf(__uint_as_float(s[q + 1])));
-  const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fabsf(k);
-  const float2 k2 = bc(k);
-  if (__all_sync(0xffffffffu, mx <= kTiny)) {
+  return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+}
+// Sets the scores of unseen pairs (bits of see) to x.
+template <int N>
+__device__ __forceinline__ void set_unseen(uint32_t* s, unsigned long long see, float x) {
+  const uint32_t w[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
-    for (int q = 0; q < N; q += 2) {
-      const float2 t = tanh_tiny2(__fmul2_rn(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), k2));
-      s[q] = __float_as_uint(t.x);
-      s[q + 1] = __float_as_uint(t.y);
-    }
-  } else if (__all_sync(0xffffffffu, mx <= kSmall)) {
-#pragma unroll
-    for (int q = 0; q < N; q += 2) {
-      const float2 t = tanh_small2(__fmul2_rn(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), k2));
-      s[q] = __float_as_uint(t.x);
-      s[q + 1] = __float_as_uint(t.y);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; q += 2) {
-      const float2 u = __fmul2_rn(make_float2(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), k2);
-      const float2 t = tanh_small2(u);
-      s[q] = __float_as_uint(fabsf(u.x) <= kSmall ? t.x : tanh_any(u.x));
-      s[q + 1] = __float_as_uint(fabsf(u.y) <= kSmall ? t.y : tanh_any(u.y));
-    }
-  }
+  for (int q = 0; q < N; ++q)
+    if (!((w[q / 32] >> (q % 32)) & 1u)) s[q] = __float_as_uint(x);
+}
+// The cheapest form that covers all of the warp's values (those of unseen
+// pairs are zero by then: what hidden rows hold picks no form).
+template <int N>
+__device__ __forceinline__ void tanh_scores(uint32_t* s, float k) {
+  const float mx = greatest<N>(s) * fabsf(k);
+  if (__all_sync(0xffffffffu, mx <= kTiny))
+    tanh_form<0, N>(s, k);
+  else if (__all_sync(0xffffffffu, mx <= kSmall))
+    tanh_form<1, N>(s, k);
+  else
+    tanh_form<2, N>(s, k);
 }
 
 // A step's key chunk as the kernels keep it: tile coordinates packed with the
@@ -109,6 +116,7 @@ constexpr uint32_t kEdge = 1u << 31;    // padded rows
 constexpr uint32_t kCausal = 1u << 30;  // some pair of the block and the chunk is hidden by time
 constexpr uint32_t kDoc = 1u << 29;     // ids differ somewhere
 constexpr uint32_t kHidden = 1u << 28;  // tokens with a negative id
+constexpr uint32_t kSpecial = kEdge | kCausal | kDoc | kHidden;
 
 struct Coord {
   int t, h, w;
@@ -156,20 +164,19 @@ __device__ __forceinline__ bool sees(const ModParams& m, int prefix, const Half&
 // step list (in place, order kept) and writes each step's packed coordinates
 // and flags to ext. One side of every pair is the block's halves (queries, or
 // keys with SWAP), the other the step's chunk. All NT threads take part;
-// returns the steps left. org (several-chunk tiles, forward) moves along.
+// returns the steps left.
 template <int NT, bool SWAP>
 __device__ __forceinline__ int filter_steps(const Geom& g, const ModParams& m, int b, int prefix, int i0, int i1, int c0,
-                                            int c1, uint32_t* list, uint32_t* ext, uint32_t* org, int steps, int* scan) {
+                                            int c1, uint32_t* list, uint32_t* ext, int steps, int* scan) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Half h0 = half_of(g, m, b, i0, c0), h1 = i1 >= 0 ? half_of(g, m, b, i1, c1) : h0;
   int kept = 0;
   for (int base = 0; base < steps; base += NT) {
     const int n = base + tid;
-    uint32_t e = 0, x = 0, og = 0;
+    uint32_t e = 0, x = 0;
     if (n < steps) {
       e = list[n];
       const int j = (int)(e & 0x1FFFFFu), c = (int)((e >> 21) & 0x1FFu);
-      if (org) og = org[n];
       const Half k = half_of(g, m, b, j, c);
       if (e >> 30 & 1u && !(SWAP ? sees(m, prefix, k, h0, &x) : sees(m, prefix, h0, k, &x))) e &= ~(1u << 30);
       if (e >> 31 & 1u && !(SWAP ? sees(m, prefix, k, h1, &x) : sees(m, prefix, h1, k, &x))) e &= ~(1u << 31);
@@ -193,7 +200,6 @@ __device__ __forceinline__ int filter_steps(const Geom& g, const ModParams& m, i
     if (keep) {  // pos <= n: no entry of a later round is overwritten
       list[pos] = e;
       ext[pos] = x;
-      if (org) org[pos] = og;
     }
   }
   return kept;
@@ -274,62 +280,73 @@ __device__ __forceinline__ unsigned long long visible_doc(const ModParams& m, si
   return vis;
 }
 
-// y[q] += sum over the axes of nw[a] |at[a] - d[a][first + q]|: the distance
-// bias of a token at offset `at` from the chunk's first token, or, with y = 0
-// and positive weights, the distance itself. In chunks whose rows of four lie
-// along w (cw a multiple of 4) the t and h terms are one value for four
-// columns, and cw = 4 leaves four w terms per step: 3 operations a column
-// against 6.75 for axis after axis. Axes of weight zero or of one token are
-// passed over.
+// Distance bias of a token at offset (t, h, w) from the chunk's first token,
+// weights nt, nh, nw (0 for an axis of one token): y[q] += sum of weight times
+// |offset - the row's|; with y = 0 and positive weights the distance itself.
+struct Dist {
+  float t, h, w, nt, nh, nw;
+};
+__device__ __forceinline__ Dist make_dist(const Geom& g, const ModParams& m, const Coord& at, const Coord& first,
+                                          float scale) {
+  return Dist{(float)(at.t - first.t), (float)(at.h - first.h), (float)(at.w - first.w),
+              g.T > 1 ? scale * m.dist[0] : 0.f, g.H > 1 ? scale * m.dist[1] : 0.f, g.W > 1 ? scale * m.dist[2] : 0.f};
+}
+// y[q .. q + 3] += u + w terms, on packed pairs.
+__device__ __forceinline__ void add4(float* y, float u, float w0, float w1, float w2, float w3) {
+  const float2 a = __fadd2_rn(make_float2(y[0], y[1]), __fadd2_rn(bc(u), make_float2(w0, w1)));
+  const float2 b = __fadd2_rn(make_float2(y[2], y[3]), __fadd2_rn(bc(u), make_float2(w2, w3)));
+  y[0] = a.x; y[1] = a.y; y[2] = b.x; y[3] = b.y;
+}
 template <int N>
-__device__ __forceinline__ void add_distance(const Geom& g, float* y, const Table* tab, int first, const float* at,
-                                             const float* nw) {
-  if (g.cw % 4 == 0) {
-    const bool along_w = nw[2] != 0.f && g.W > 1;
-    float cw[4];
+__device__ __forceinline__ void axis_distance(float* y, const float* d, float at, float nw) {
+  const float4* d4 = reinterpret_cast<const float4*>(d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cw[i] = nw[2] * fabsf(at[2] - (float)i);
-    if (g.cw == 4 && along_w) {
+  for (int q = 0; q < N / 4; ++q) {
+    const float4 x = d4[q];
+    y[4 * q] = fmaf(fabsf(at - x.x), nw, y[4 * q]);
+    y[4 * q + 1] = fmaf(fabsf(at - x.y), nw, y[4 * q + 1]);
+    y[4 * q + 2] = fmaf(fabsf(at - x.z), nw, y[4 * q + 2]);
+    y[4 * q + 3] = fmaf(fabsf(at - x.w), nw, y[4 * q + 3]);
+  }
+}
+// In chunks whose rows of four or eight lie along w the t and h terms are one
+// value for four columns and the w terms four or eight values per step: three
+// operations a column. Chunks that are a line (sequences) take two. Axis
+// after axis, seven with the table reads, serves the other shapes and passes
+// over axes of weight zero.
+template <int N>
+__device__ __forceinline__ void add_distance(const Geom& g, float* y, const Table* tab, int first, const Dist& p) {
+  if (g.cw == 4 || g.cw == 8) {
+    float w[8];
 #pragma unroll
-      for (int q = 0; q < N / 4; ++q) {
-        const float4 d = tab->group[first / 4 + q];
-        const float u = fmaf(nw[1], fabsf(at[1] - d.y), nw[0] * fabsf(at[0] - d.x));
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float2 r = __fadd2_rn(make_float2(y[4 * q + i], y[4 * q + i + 1]), __fadd2_rn(bc(u), make_float2(cw[i], cw[i + 1])));
-          y[4 * q + i] = r.x;
-          y[4 * q + i + 1] = r.y;
-        }
-      }
-      return;
-    }
+    for (int i = 0; i < 8; ++i) w[i] = p.nw * fabsf(p.w - (float)i);
+    const bool wide = g.cw == 8;
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) {
-      const float4 d = tab->group[first / 4 + q];
-      const float u = fmaf(nw[1], fabsf(at[1] - d.y), nw[0] * fabsf(at[0] - d.x));
-      const float w = at[2] - d.z;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[4 * q + i] += u;
-        if (along_w) y[4 * q + i] = fmaf(nw[2], fabsf(w - (float)i), y[4 * q + i]);
-      }
+      const float2 d = *reinterpret_cast<const float2*>(&tab->group[first / 4 + q]);
+      const float u = fmaf(p.nh, fabsf(p.h - d.y), p.nt * fabsf(p.t - d.x));
+      if ((q & 1) && wide)
+        add4(y + 4 * q, u, w[4], w[5], w[6], w[7]);
+      else
+        add4(y + 4 * q, u, w[0], w[1], w[2], w[3]);
     }
     return;
   }
-  const int extent[3] = {g.T, g.H, g.W};
+  if (g.ct == 64 || g.cw == 64) {  // 64 tokens in a line along t or w: the offset is the column
+    const float at = g.ct == 64 ? p.t : p.w, n = g.ct == 64 ? p.nt : p.nw;
+    const float u = fmaf(p.nh, fabsf(p.h), g.ct == 64 ? p.nw * fabsf(p.w) : p.nt * fabsf(p.t));
+    const float a0 = at - (float)first;
 #pragma unroll
-  for (int a = 0; a < 3; ++a) {
-    if (nw[a] == 0.f || extent[a] == 1) continue;
-    const float4* d4 = reinterpret_cast<const float4*>(tab->d[a] + first);
+    for (int q = 0; q < N; ++q) y[q] = fmaf(fabsf(a0 - (float)q), n, y[q]);
+    if (u != 0.f) {
 #pragma unroll
-    for (int q = 0; q < N / 4; ++q) {
-      const float4 d = d4[q];
-      y[4 * q] = fmaf(fabsf(at[a] - d.x), nw[a], y[4 * q]);
-      y[4 * q + 1] = fmaf(fabsf(at[a] - d.y), nw[a], y[4 * q + 1]);
-      y[4 * q + 2] = fmaf(fabsf(at[a] - d.z), nw[a], y[4 * q + 2]);
-      y[4 * q + 3] = fmaf(fabsf(at[a] - d.w), nw[a], y[4 * q + 3]);
+      for (int q = 0; q < N; ++q) y[q] += u;
     }
+    return;
   }
+  if (p.nt != 0.f) axis_distance<N>(y, tab->d[0] + first, p.t, p.nt);
+  if (p.nh != 0.f) axis_distance<N>(y, tab->d[1] + first, p.h, p.nh);
+  if (p.nw != 0.f) axis_distance<N>(y, tab->d[2] + first, p.w, p.nw);
 }
 
 // Zeroes a 64-row operand tile's rows of hidden tokens (128-byte swizzle: a
