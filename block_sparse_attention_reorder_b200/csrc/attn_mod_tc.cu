@@ -111,6 +111,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params P) {
   using C = Cfg<D, FP8>;
+  // Cap and bias together: 32 columns at a time in a loop, with P in two
+  // halves (16 columns each, 32 apart). Straight-line code for all 64 stalls
+  // on instruction fetch (PLACEHOLDER).
+  constexpr bool kSplit = CAP && BIAS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -364,7 +368,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t dv = tc::smem_desc(sb + C::OFF_V + s * C::V_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
-          tc::mma_ts_f16(tmem + kColO, pA + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_ts_f16(tmem + kColO, pA + (kSplit && kk >= 2 ? 16 : 0) + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
         }
         tc::mma_commit(bar_pvdone(n & 1));
         if (n + 2 < L && !issue_S(n + 2)) {
@@ -457,62 +461,119 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t sbuf = tmem + lane_base + ((n & 1) ? kColS1 : kColS0);
-      uint32_t pk[32];
-      float alpha = 1.f;
-      if (keep) {
-        const float c = FP8 && !CAP ? c_fix * ksc : c_fix, k = FP8 ? kq * ksc : kq;
-        float sum;
-        uint32_t sr[64];
-        // P and its sum from the modified scores.
-        auto exponentials = [&]() {
-          // A row that has seen no key yet has m = -inf and only -inf scores.
-          const float2 c2 = mod::bc(c), nm2 = mod::bc(m == -INFINITY ? 0.f : -m);
-          float2 ls2[4] = {mod::bc(0.f), mod::bc(0.f), mod::bc(0.f), mod::bc(0.f)};
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            const float2 x = __ffma2_rn(mod::pair(sr + 2 * q), c2, nm2);
-            const float2 p = make_float2(tc::ex2(x.x), tc::ex2(x.y));
-            ls2[q & 3] = __fadd2_rn(ls2[q & 3], p);
-            pk[q] = mod::pack(p);
-          }
-          const float2 ls = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
-          sum = ls.x + ls.y;
-        };
-        // Once more with the row maxima when a score turns out to be far above
-        // its row's reference.
-        bool done = false;
-        for (bool measure = fresh; !done; measure = true) {
-          tc::tmem_ld64_wait(sbuf, sr);
-          if (CAP) {
-            if (partial) mod::set_unseen<64>(sr, vis, 0.f);
-            mod::tanh_scores<64>(sr, k);
-          }
-          if (BIAS) mod::add_distance<64>(g, reinterpret_cast<float*>(sr), &tab->col, 0, dist);
-          if (partial) mod::set_unseen<64>(sr, vis, -INFINITY);
-          if (measure) {
+      if constexpr (kSplit) {
+        const float k = FP8 ? kq * ksc : kq;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+          if (keep) {
+            uint32_t sr[32];
+            const uint32_t see = (uint32_t)(vis >> (32 * h));
+            tc::tmem_ld32_wait(sbuf + 32 * h, sr);
+            if (partial) mod::set_unseen<32>(sr, see, 0.f);
+            mod::tanh_scores<32>(sr, k);
+            mod::add_distance<32>(g, reinterpret_cast<float*>(sr), &tab->col, 32 * h, dist);
+            if (partial) mod::set_unseen<32>(sr, see, -INFINITY);
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int q = 0; q < 32; ++q)
+            for (int q = 0; q < 16; ++q)
               mx4[q & 3] = tc::fmax3(mx4[q & 3], __uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1]));
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
-            if (mx > m + kRaise) {  // m = -inf: the row has seen no key and its O row is zero
-              if (m != -INFINITY) alpha = tc::ex2(m - (mx + kAbove));
-              m = mx + kAbove;
-            }
-            fresh = __any_sync(0xffffffffu, m == -INFINITY);
-          }
-          exponentials();
-          done = measure || __all_sync(0xffffffffu, sum <= kSumLimit);
-        }
-        l = l * alpha + sum;
-      } else {
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c_fix;
+            const bool raise = mx > m + kRaise;  // m = -inf: the row has seen no key and its O row is zero
+            if (__any_sync(0xffffffffu, raise)) {
+              const float alpha = raise && m != -INFINITY ? tc::ex2(m - (mx + kAbove)) : 1.f;
+              if (raise) m = mx + kAbove;
+              if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                l *= alpha;
+                if (n > 0) ok = rescale(n, alpha);
+                if (h == 1) {  // this step's first 32 probabilities
+                  tc::tmem_ld16_wait(sbuf, pk);
 #pragma unroll
-        for (int q = 0; q < 32; ++q) pk[q] = 0u;
-      }
-      tc::tmem_st32(sbuf, pk);  // P_n over the first 32 columns of S_n
-      if (__any_sync(0xffffffffu, alpha != 1.f) && !rescale(n, alpha)) {
-        ok = false;
-        break;
+                  for (int q = 0; q < 16; ++q) {
+                    const float2 p = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&pk[q]));
+                    pk[q] = mod::pack(make_float2(p.x * alpha, p.y * alpha));
+                  }
+                  tc::tmem_st16(sbuf, pk);
+                }
+              }
+            }
+            // A row that has seen no key yet has m = -inf and only -inf scores.
+            const float2 c2 = mod::bc(c_fix), nm2 = mod::bc(m == -INFINITY ? 0.f : -m);
+            float2 ls2[2] = {mod::bc(0.f), mod::bc(0.f)};
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float2 x = __ffma2_rn(mod::pair(sr + 2 * q), c2, nm2);
+              const float2 p = make_float2(tc::ex2(x.x), tc::ex2(x.y));
+              ls2[q & 1] = __fadd2_rn(ls2[q & 1], p);
+              pk[q] = mod::pack(p);
+            }
+            const float2 ls = __fadd2_rn(ls2[0], ls2[1]);
+            l += ls.x + ls.y;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) pk[q] = 0u;
+          }
+          tc::tmem_st16(sbuf + 32 * h, pk);  // P over the first 16 columns of its half of S_n
+        }
+        if (!ok) break;
+      } else {
+        uint32_t pk[32];
+        float alpha = 1.f;
+        if (keep) {
+          const float c = FP8 && !CAP ? c_fix * ksc : c_fix, k = FP8 ? kq * ksc : kq;
+          float sum;
+          uint32_t sr[64];
+          // P and its sum from the modified scores.
+          auto exponentials = [&]() {
+            // A row that has seen no key yet has m = -inf and only -inf scores.
+            const float2 c2 = mod::bc(c), nm2 = mod::bc(m == -INFINITY ? 0.f : -m);
+            float2 ls2[4] = {mod::bc(0.f), mod::bc(0.f), mod::bc(0.f), mod::bc(0.f)};
+  #pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float2 x = __ffma2_rn(mod::pair(sr + 2 * q), c2, nm2);
+              const float2 p = make_float2(tc::ex2(x.x), tc::ex2(x.y));
+              ls2[q & 3] = __fadd2_rn(ls2[q & 3], p);
+              pk[q] = mod::pack(p);
+            }
+            const float2 ls = __fadd2_rn(__fadd2_rn(ls2[0], ls2[1]), __fadd2_rn(ls2[2], ls2[3]));
+            sum = ls.x + ls.y;
+          };
+          // Once more with the row maxima when a score turns out to be far above
+          // its row's reference.
+          bool done = false;
+          for (bool measure = fresh; !done; measure = true) {
+            tc::tmem_ld64_wait(sbuf, sr);
+            if (CAP) {
+              if (partial) mod::set_unseen<64>(sr, vis, 0.f);
+              mod::tanh_scores<64>(sr, k);
+            }
+            if (BIAS) mod::add_distance<64>(g, reinterpret_cast<float*>(sr), &tab->col, 0, dist);
+            if (partial) mod::set_unseen<64>(sr, vis, -INFINITY);
+            if (measure) {
+              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  #pragma unroll
+              for (int q = 0; q < 32; ++q)
+                mx4[q & 3] = tc::fmax3(mx4[q & 3], __uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1]));
+              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+              if (mx > m + kRaise) {  // m = -inf: the row has seen no key and its O row is zero
+                if (m != -INFINITY) alpha = tc::ex2(m - (mx + kAbove));
+                m = mx + kAbove;
+              }
+              fresh = __any_sync(0xffffffffu, m == -INFINITY);
+            }
+            exponentials();
+            done = measure || __all_sync(0xffffffffu, sum <= kSumLimit);
+          }
+          l = l * alpha + sum;
+        } else {
+  #pragma unroll
+          for (int q = 0; q < 32; ++q) pk[q] = 0u;
+        }
+        tc::tmem_st32(sbuf, pk);  // P_n over the first 32 columns of S_n
+        if (__any_sync(0xffffffffu, alpha != 1.f) && !rescale(n, alpha)) {
+          ok = false;
+          break;
+        }
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();

@@ -17,10 +17,11 @@ constexpr int kHiddenDoc = -2;  // a query id that equals no key's
 
 // tanh for small |u|: u (1 + v P(v)), v = u^2, P fitted to (tanh(u) / u - 1)
 // / v for the least maximum relative error of tanh (Lawson's iteratively
-// reweighted least squares): degree 4 on |u| <= 0.75 (3.2e-8; 1.0e-7 with
-// fp32 evaluation), degree 2 on |u| <= 0.375 (7.0e-8; 1.3e-7). Six and eight
-// FMA-pipe operations on packed pairs, the SFU stays free for the softmax.
-constexpr float kSmall = 0.75f, kTiny = 0.375f;
+// reweighted least squares): degree 2 on |u| <= 0.375 (7.0e-8; 1.3e-7 with
+// fp32 evaluation), degree 4 on |u| <= 0.75 (3.2e-8; 1.0e-7), degree 7 on |u|
+// <= 1.5 (1.2e-7; 3.0e-7). Six, eight and eleven FMA-pipe operations on
+// packed pairs; the SFU stays free for the softmax.
+constexpr float kTiny = 0.375f, kSmall = 0.75f, kWide = 1.5f;
 __device__ __forceinline__ float2 bc(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 pair(const uint32_t* r) { return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 __device__ __forceinline__ uint32_t pack(float2 v) {
@@ -55,6 +56,17 @@ __device__ __forceinline__ float2 tanh_small2(float2 u) {
   p = __ffma2_rn(p, v, bc(-0.3333306908607483f));
   return __fmul2_rn(u, __ffma2_rn(p, v, bc(1.f)));
 }
+__device__ __forceinline__ float2 tanh_wide2(float2 u) {
+  const float2 v = __fmul2_rn(u, u);
+  float2 p = __ffma2_rn(bc(2.621273961267434e-05f), v, bc(-0.000327014276990667f));
+  p = __ffma2_rn(p, v, bc(0.0018979610176756978f));
+  p = __ffma2_rn(p, v, bc(-0.007121095899492502f));
+  p = __ffma2_rn(p, v, bc(0.0207283403724432f));
+  p = __ffma2_rn(p, v, bc(-0.053532831370830536f));
+  p = __ffma2_rn(p, v, bc(0.13325031101703644f));
+  p = __ffma2_rn(p, v, bc(-0.3333278000354767f));
+  return __fmul2_rn(u, __ffma2_rn(p, v, bc(1.f)));
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -67,17 +79,20 @@ __device__ __forceinline__ float tanh_any(float u) {
 }
 
 // Replaces raw scores s[] by tanh(k s) (k = scale / cap) in the form that TIER
-// names: 0 and 1 the polynomials, 2 the polynomial where |u| is small (most
-// values even under a low cap: the branch is seldom taken) and else the SFU
-// form. The forms agree to about 2e-7 of the value.
+// names: 0, 1 and 2 the polynomials, 3 the SFU form. The forms agree to about
+// 3e-7 absolute.
 template <int TIER, int N>
 __device__ __forceinline__ void tanh_form(uint32_t* s, float k) {
   const float2 k2 = bc(k);
 #pragma unroll
   for (int q = 0; q < N; q += 2) {
-    const float2 u = __fmul2_rn(pair(s + q), k2), t = TIER == 0 ? tanh_tiny2(u) : tanh_small2(u);
-    s[q] = __float_as_uint(TIER < 2 || fabsf(u.x) <= kSmall ? t.x : tanh_any(u.x));
-    s[q + 1] = __float_as_uint(TIER < 2 || fabsf(u.y) <= kSmall ? t.y : tanh_any(u.y));
+    const float2 u = __fmul2_rn(pair(s + q), k2);
+    const float2 t = TIER == 0   ? tanh_tiny2(u)
+                     : TIER == 1 ? tanh_small2(u)
+                     : TIER == 2 ? tanh_wide2(u)
+                                 : make_float2(tanh_any(u.x), tanh_any(u.y));
+    s[q] = __float_as_uint(t.x);
+    s[q + 1] = __float_as_uint(t.y);
   }
 }
 // Greatest |s|; a NaN is passed over.
@@ -106,8 +121,10 @@ __device__ __forceinline__ void tanh_scores(uint32_t* s, float k) {
     tanh_form<0, N>(s, k);
   else if (__all_sync(0xffffffffu, mx <= kSmall))
     tanh_form<1, N>(s, k);
-  else
+  else if (__all_sync(0xffffffffu, mx <= kWide))
     tanh_form<2, N>(s, k);
+  else
+    tanh_form<3, N>(s, k);
 }
 
 // A step's key chunk as the kernels keep it: tile coordinates packed with the
