@@ -2,20 +2,22 @@
 //
 // Pair (x, y) of a token at position pos turns by pos * f (f per pair):
 //   (x, y) -> m (x cos - y sin, x sin + y cos),
-// the transpose with -sin. The angle is formed in turns in fp64 (pos * f / 2pi
-// minus its nearest integer), so that far positions keep fp32's accuracy in
-// sine and cosine; one rounding to bf16 at the end.
+// the transpose with -sin. f / 2 pi is a 64-bit binary fraction, so that
+// pos * f wraps modulo one turn by itself in integer arithmetic, exactly for
+// every int32 position; its upper 32 bits go to fp32 sine and cosine. One
+// rounding to bf16 at the end.
 //
-// Memory bound: every tensor is read and written once. A CTA takes one 64-row
-// chunk of a tile (with tile means: one tile, chunk by chunk) and a block of
-// columns of the token rows, thread c owning the same features of every row,
-// so that rows are read coalesced, a pair's two features meet in one thread
-// (in-place calls are safe) and the tile's sum needs no exchange. Angles
-// depend on a row only through its coordinate along the pair's axis: the CTA
-// fills a shared table [coordinate within the chunk's box][pair] of (cos, sin)
-// once, at most 64 x 64 entries (12 x 21 for a (4, 4, 4) chunk), instead of
-// one sine per token, pair and head. Explicit positions give one table row
-// per token row.
+// Memory bound: every tensor is read and written once. Angles depend on a row
+// only through its coordinate along the pair's axis: a CTA takes one 64-row
+// chunk of a tile (with tile means: one tile, chunk by chunk) and a few heads,
+// and fills a shared table [coordinate within the chunk's box][pair] of (cos,
+// sin), 4 x 64 entries for a (4, 4, 4) chunk and at most 64 x 64. Explicit
+// positions give one table row per token row. A thread owns the same features
+// (its unit) of every rg-th row and of kHeads heads: the angles it reads from
+// the table serve all of its heads, a pair's two features meet in one thread
+// (in-place calls are safe), and its share of a tile's sum stays in
+// registers until one exchange at the end, in a fixed order.
+// PLACEHOLDER
 #include "internal.h"
 
 #include <math.h>
@@ -36,9 +38,10 @@ struct RopeParams {
   int split[2];         // first pair of the h and w axes
   float amp;
   float sign;           // -1: transposed rotation
-  int ncblk;            // column blocks per tensor
+  int hblk;             // head blocks per tensor
   int by_tile;          // a CTA takes a whole tile (tile means)
-  double turns[64];     // f / (2 pi) of each pair
+  int nu, rg;           // units per head, rows taken at once
+  unsigned long long turns[64];  // f / (2 pi) modulo 1, in 2^-64
 };
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -50,38 +53,40 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// What a thread owns of every token row. Units are numbered over a head's
-// features, then heads:
+// A unit, what a thread owns of a head:
 //   kInterleaved: 8 neighbouring features (4 pairs)                  D / 8 units
 //   kHalf8:       features [8u, 8u + 8) and [R + 8u, R + 8u + 8) (8
 //                 pairs), R a multiple of 8; 8 passed features each   (D - R) / 8 units
 //   kPair:        two features: a pair, or two passed ones; for half
 //                 layouts whose R is not a multiple of 8 (2-byte
 //                 accesses: 4x the load instructions of kHalf8)       D / 2 units
-constexpr uint32_t kHiddenRow = 1u << 31;
 enum Mode { kInterleaved, kHalf8, kPair };
+constexpr int kHeads = 4;  // heads of a CTA
+constexpr uint32_t kHiddenRow = 1u << 31;
 
 template <int MODE, bool POOL>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(const __grid_constant__ RopeParams P) {
-  constexpr int NV = MODE == kPair ? 2 : MODE == kHalf8 ? 16 : 8;  // features a thread owns
+  constexpr int NV = MODE == kPair ? 2 : MODE == kHalf8 ? 16 : 8;  // features of a unit
   constexpr int NP = NV / 2;
-  constexpr int kRowsInFlight = MODE == kHalf8 ? 4 : 8;  // eight 16-byte loads in flight a thread
+  constexpr int kRows = MODE == kHalf8 ? 1 : 2;                    // rows in flight: eight 16-byte loads a thread
   extern __shared__ float2 table[];   // [value][pair]
   __shared__ int rowtok[64];          // token of each row of the chunk, -1 for a padded slot
   __shared__ uint32_t rowval[64];     // its table rows along t, h, w; kHiddenRow set for a hidden token
+  __shared__ int seen;                // tokens in the sums
+  __shared__ float part[POOL ? kThreads * kHeads * NV : 1];
   const Geom& g = P.g;
-  const int D = g.D, R = P.npairs;
-  const int tensor = blockIdx.z / P.ncblk, cblk = blockIdx.z % P.ncblk, b = blockIdx.y;
-  const int j = P.by_tile ? blockIdx.x : blockIdx.x / g.nchunk;
-  const int ch0 = P.by_tile ? 0 : blockIdx.x % g.nchunk, ch1 = P.by_tile ? g.nchunk : ch0 + 1;
+  const int D = g.D, R = P.npairs, tid = threadIdx.x;
+  // Head blocks vary fastest, so that CTAs that run together read whole token
+  // rows (all heads of a token are contiguous).
+  const int tensor = blockIdx.z, b = blockIdx.y, head0 = blockIdx.x % P.hblk * kHeads, item = blockIdx.x / P.hblk;
+  const int j = P.by_tile ? item : item / g.nchunk;
+  const int ch0 = P.by_tile ? 0 : item % g.nchunk, ch1 = P.by_tile ? g.nchunk : ch0 + 1;
   const __nv_bfloat16* x = P.x[tensor];
   __nv_bfloat16* y = P.y[tensor];
   const int bt = j / (g.nH * g.nW), bh = (j / g.nW) % g.nH, bw = j % g.nW;
-  const int nu = MODE == kInterleaved ? D / 8 : MODE == kHalf8 ? (D - R) / 8 : D / 2;
-  const int unit = cblk * kThreads + threadIdx.x;
-  const int head = unit / nu, u = unit % nu;
-  const bool active = head < g.Hh;
+  const int u = tid % P.nu, grp = tid / P.nu;
+  const bool active = grp < P.rg;
   // First feature of each part, first pair (-1: passed unchanged).
   int fa, fb = 0, p0;
   if (MODE == kInterleaved) {
@@ -99,13 +104,20 @@ rope_kernel(const __grid_constant__ RopeParams P) {
     p0 = turned ? u : -1;
   }
   const int np = p0 < 0 ? 0 : min(NP, R - p0);  // turned pairs among the thread's (interleaved: a unit may end mid-way)
+  // Shift that takes a pair's axis out of rowval.
+  uint32_t shift[NP];
+#pragma unroll
+  for (int e = 0; e < NP; ++e) shift[e] = p0 + e < P.split[0] ? 0 : p0 + e < P.split[1] ? 8 : 16;
   const size_t row_el = (size_t)g.Hh * D;
-  const size_t base = (size_t)b * g.L * row_el + (size_t)head * D;
-  float acc[POOL ? NV : 1];
-  int seen = 0;  // tokens in the sums
+  const size_t base = (size_t)b * g.L * row_el + (size_t)head0 * D;
+  const int nh = min(kHeads, g.Hh - head0);
+  float acc[POOL ? kHeads : 1][POOL ? NV : 1];
   if (POOL) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) acc[e] = 0.f;
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) acc[h][e] = 0.f;
+    if (tid == 0) seen = 0;
   }
 
   for (int ch = ch0; ch < ch1; ++ch) {
@@ -113,151 +125,169 @@ rope_kernel(const __grid_constant__ RopeParams P) {
     const int t0 = bt * g.tt + o.dt, h0 = bh * g.th + o.dh, w0 = bw * g.tw + o.dw;
     if (t0 >= g.T || h0 >= g.H || w0 >= g.W) continue;  // padding only (uniform over the CTA)
     __syncthreads();  // the previous chunk's table and rows are read
-    if (threadIdx.x < 64) {
-      const uint32_t cc = chunk_row_code(g, threadIdx.x);
+    if (tid < 64) {
+      const uint32_t cc = chunk_row_code(g, tid);
       const int t = t0 + (int)(cc & 0xffu), h = h0 + (int)((cc >> 8) & 0xffu), w = w0 + (int)((cc >> 16) & 0xffu);
-      const bool real = threadIdx.x < g.cr && t < g.T && h < g.H && w < g.W;
-      rowtok[threadIdx.x] = real ? (t * g.H + h) * g.W + w : -1;
-      uint32_t val = P.pos ? (uint32_t)threadIdx.x * 0x10101u : cc;
-      if (P.doc && real && P.doc[(size_t)b * g.L + (t * g.H + h) * g.W + w] < 0) val |= kHiddenRow;
-      rowval[threadIdx.x] = val;
-    }
-    __syncthreads();
-    const int vals = P.pos ? 64 : max(g.ct, max(g.ch, g.cw));
-    for (int e = threadIdx.x; e < vals * R; e += kThreads) {
-      const int v = e / R, p = e % R;
-      const int a = p < P.split[0] ? 0 : p < P.split[1] ? 1 : 2;
-      double at;
-      if (P.pos) {
-        const int n = rowtok[v];
-        if (n < 0) continue;
-        at = (double)P.pos[((size_t)b * g.L + n) * 3 + a];
-      } else {
-        if (v >= (a == 0 ? g.ct : a == 1 ? g.ch : g.cw)) continue;
-        at = (double)P.off[a] + (double)((a == 0 ? t0 : a == 1 ? h0 : w0) + v);
+      const bool real = tid < g.cr && t < g.T && h < g.H && w < g.W;
+      const int n = real ? (t * g.H + h) * g.W + w : -1;
+      uint32_t val = P.pos ? (uint32_t)tid * 0x10101u : cc;
+      if (P.doc && real && P.doc[(size_t)b * g.L + n] < 0) val |= kHiddenRow;
+      rowtok[tid] = n;
+      rowval[tid] = val;
+      if (POOL) {
+        const uint32_t in = __ballot_sync(0xffffffffu, real && !(val & kHiddenRow));
+        if (tid % 32 == 0) atomicAdd(&seen, __popc(in));
       }
-      double turn = at * P.turns[p];
-      turn -= rint(turn);
-      float s, c;
-      sincospif((float)(2.0 * turn), &s, &c);
-      table[v * R + p] = make_float2(c * P.amp, s * P.amp * P.sign);
+    }
+    if (P.pos) __syncthreads();
+    // The table: thread tid takes pair tid % 64 of every second value.
+    const int p = tid % 64;
+    if (p < R) {
+      const int a = p < P.split[0] ? 0 : p < P.split[1] ? 1 : 2;
+      const int vals = P.pos ? g.cr : a == 0 ? g.ct : a == 1 ? g.ch : g.cw;
+      const unsigned long long f = P.turns[p];
+      const long long at0 = (long long)P.off[a] + (a == 0 ? t0 : a == 1 ? h0 : w0);
+      for (int v = tid / 64; v < vals; v += kThreads / 64) {
+        long long at = at0 + v;
+        if (P.pos) {
+          const int n = rowtok[v];
+          if (n < 0) continue;
+          at = P.pos[((size_t)b * g.L + n) * 3 + a];
+        }
+        const int hi = (int)(((unsigned long long)at * f) >> 32);  // the turn in [-1/2, 1/2), in 2^-32
+        float s, c;
+        sincospif((float)hi * 0x1p-31f, &s, &c);
+        table[v * R + p] = make_float2(c * P.amp, s * P.amp * P.sign);
+      }
     }
     __syncthreads();
     if (!active) continue;
 #pragma unroll 1
-    for (int r0 = 0; r0 < g.cr; r0 += kRowsInFlight) {
-      uint4 va[kRowsInFlight], vb[MODE == kHalf8 ? kRowsInFlight : 1];
-      float sa[MODE == kPair ? kRowsInFlight : 1], sb[MODE == kPair ? kRowsInFlight : 1];
+    for (int r0 = grp; r0 < g.cr; r0 += kRows * P.rg) {
+      uint4 va[kRows][kHeads], vb[MODE == kHalf8 ? kRows : 1][kHeads];
+      float sa[MODE == kPair ? kRows : 1][kHeads], sb[MODE == kPair ? kRows : 1][kHeads];
+      int tok[kRows];
 #pragma unroll
-      for (int i = 0; i < kRowsInFlight; ++i) {
-        const int n = r0 + i < g.cr ? rowtok[r0 + i] : -1;
-        if (n < 0) continue;
-        const __nv_bfloat16* src = x + base + (size_t)n * row_el;
-        if (MODE == kPair) {
-          sa[i] = __bfloat162float(src[fa]);
-          sb[i] = __bfloat162float(src[fb]);
-        } else {
-          va[i] = *reinterpret_cast<const uint4*>(src + fa);
-          if (MODE == kHalf8 && p0 >= 0) vb[i] = *reinterpret_cast<const uint4*>(src + fb);
+      for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i * P.rg;
+        tok[i] = r < g.cr ? rowtok[r] : -1;
+        if (tok[i] < 0) continue;
+        const __nv_bfloat16* src = x + base + (size_t)tok[i] * row_el;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          if (h >= nh) continue;
+          if (MODE == kPair) {
+            sa[i][h] = __bfloat162float(src[h * D + fa]);
+            sb[i][h] = __bfloat162float(src[h * D + fb]);
+          } else {
+            va[i][h] = *reinterpret_cast<const uint4*>(src + h * D + fa);
+            if (MODE == kHalf8 && p0 >= 0) vb[i][h] = *reinterpret_cast<const uint4*>(src + h * D + fb);
+          }
         }
       }
 #pragma unroll
-      for (int i = 0; i < kRowsInFlight; ++i) {
-        const int n = r0 + i < g.cr ? rowtok[r0 + i] : -1;
-        if (n < 0) continue;
-        const uint32_t val = rowval[r0 + i];
-        if (val & kHiddenRow) {  // zeros, whatever the row holds
-          if (MODE == kPair) {
-            sa[i] = sb[i] = 0.f;
-          } else {
-            va[i] = make_uint4(0, 0, 0, 0);
-            if (MODE == kHalf8) vb[i] = make_uint4(0, 0, 0, 0);
-          }
-        } else {
-          ++seen;
-        }
-        auto turn = [&](int p) -> float2 {
-          const uint32_t v = p < P.split[0] ? val & 0xffu : p < P.split[1] ? (val >> 8) & 0xffu : (val >> 16) & 0xffu;
-          return table[v * R + p];
-        };
-        __nv_bfloat16* dst = y + base + (size_t)n * row_el;
-        float f[NV];
-        if (MODE == kPair) {
-          f[0] = sa[i];
-          f[1] = sb[i];
-          if (np) {
-            const float2 cs = turn(p0);
-            f[0] = sa[i] * cs.x - sb[i] * cs.y;
-            f[1] = sa[i] * cs.y + sb[i] * cs.x;
-          }
-          dst[fa] = __float2bfloat16_rn(f[0]);
-          dst[fb] = __float2bfloat16_rn(f[1]);
-        } else if (MODE == kInterleaved) {
-          const uint32_t w[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
-          uint32_t q[4];
+      for (int i = 0; i < kRows; ++i) {
+        if (tok[i] < 0) continue;
+        const uint32_t val = rowval[r0 + i * P.rg];
+        float2 cs[NP];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack2(w[e]);
-            f[2 * e] = a.x;
-            f[2 * e + 1] = a.y;
-            if (e < np) {
-              const float2 cs = turn(p0 + e);
-              f[2 * e] = a.x * cs.x - a.y * cs.y;
-              f[2 * e + 1] = a.x * cs.y + a.y * cs.x;
+        for (int e = 0; e < NP; ++e)
+          cs[e] = e < np ? table[((val >> shift[e]) & 0xffu) * R + p0 + e] : make_float2(1.f, 0.f);
+        __nv_bfloat16* dst = y + base + (size_t)tok[i] * row_el;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          if (h >= nh) continue;
+          if (val & kHiddenRow) {  // zeros, whatever the row holds
+            if (MODE == kPair) {
+              sa[i][h] = sb[i][h] = 0.f;
+            } else {
+              va[i][h] = make_uint4(0, 0, 0, 0);
+              if (MODE == kHalf8) vb[i][h] = make_uint4(0, 0, 0, 0);
             }
-            q[e] = pack2(f[2 * e], f[2 * e + 1]);
           }
-          *reinterpret_cast<uint4*>(dst + fa) = make_uint4(q[0], q[1], q[2], q[3]);
-        } else {
-          const uint32_t w[4] = {va[i].x, va[i].y, va[i].z, va[i].w};
-          if (p0 < 0) {
+          float f[NV];
+          if (MODE == kPair) {
+            f[0] = np ? sa[i][h] * cs[0].x - sb[i][h] * cs[0].y : sa[i][h];
+            f[1] = np ? sa[i][h] * cs[0].y + sb[i][h] * cs[0].x : sb[i][h];
+            dst[h * D + fa] = __float2bfloat16_rn(f[0]);
+            dst[h * D + fb] = __float2bfloat16_rn(f[1]);
+          } else if (MODE == kInterleaved) {
+            const uint32_t w[4] = {va[i][h].x, va[i][h].y, va[i][h].z, va[i][h].w};
+            uint32_t q[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 a = unpack2(w[e]);
               f[2 * e] = a.x;
               f[2 * e + 1] = a.y;
-            }
-            *reinterpret_cast<uint4*>(dst + fa) = va[i];
-          } else {
-            const uint32_t z[4] = {vb[i].x, vb[i].y, vb[i].z, vb[i].w};
-            uint32_t q[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 a = unpack2(w[e]), c = unpack2(z[e]);
-              const float2 k0 = turn(p0 + 2 * e), k1 = turn(p0 + 2 * e + 1);
-              f[2 * e] = a.x * k0.x - c.x * k0.y;
-              f[2 * e + 1] = a.y * k1.x - c.y * k1.y;
-              f[(8 + 2 * e) % NV] = a.x * k0.y + c.x * k0.x;
-              f[(9 + 2 * e) % NV] = a.y * k1.y + c.y * k1.x;
+              if (e < np) {  // not by cos 1, sin 0: 0 * inf
+                f[2 * e] = a.x * cs[e].x - a.y * cs[e].y;
+                f[2 * e + 1] = a.x * cs[e].y + a.y * cs[e].x;
+              }
               q[e] = pack2(f[2 * e], f[2 * e + 1]);
-              q[4 + e] = pack2(f[(8 + 2 * e) % NV], f[(9 + 2 * e) % NV]);
             }
-            *reinterpret_cast<uint4*>(dst + fa) = make_uint4(q[0], q[1], q[2], q[3]);
-            *reinterpret_cast<uint4*>(dst + fb) = make_uint4(q[4], q[5], q[6], q[7]);
-          }
-        }
-        if (POOL) {
+            *reinterpret_cast<uint4*>(dst + h * D + fa) = make_uint4(q[0], q[1], q[2], q[3]);
+          } else {
+            const uint32_t w[4] = {va[i][h].x, va[i][h].y, va[i][h].z, va[i][h].w};
+            if (p0 < 0) {
 #pragma unroll
-          for (int e = 0; e < NV; ++e)
-            if (MODE != kHalf8 || e < 8 || p0 >= 0) acc[e] += f[e];
+              for (int e = 0; e < 4; ++e) {
+                const float2 a = unpack2(w[e]);
+                f[2 * e] = a.x;
+                f[2 * e + 1] = a.y;
+              }
+              *reinterpret_cast<uint4*>(dst + h * D + fa) = va[i][h];
+            } else {
+              const uint32_t z[4] = {vb[i][h].x, vb[i][h].y, vb[i][h].z, vb[i][h].w};
+              uint32_t q[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 a = unpack2(w[e]), c = unpack2(z[e]);
+                const float2 k0 = cs[(2 * e) % NP], k1 = cs[(2 * e + 1) % NP];
+                f[2 * e] = a.x * k0.x - c.x * k0.y;
+                f[2 * e + 1] = a.y * k1.x - c.y * k1.y;
+                f[(8 + 2 * e) % NV] = a.x * k0.y + c.x * k0.x;
+                f[(9 + 2 * e) % NV] = a.y * k1.y + c.y * k1.x;
+                q[e] = pack2(f[2 * e], f[2 * e + 1]);
+                q[4 + e] = pack2(f[(8 + 2 * e) % NV], f[(9 + 2 * e) % NV]);
+              }
+              *reinterpret_cast<uint4*>(dst + h * D + fa) = make_uint4(q[0], q[1], q[2], q[3]);
+              *reinterpret_cast<uint4*>(dst + h * D + fb) = make_uint4(q[4], q[5], q[6], q[7]);
+            }
+          }
+          if (POOL) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+              if (MODE != kHalf8 || e < 8 || p0 >= 0) acc[h][e] += f[e];
+          }
         }
       }
     }
   }
-  if (POOL && active) {
-    const float n = (float)max(seen, 1);
-    float* out = P.pooled[tensor] + (((size_t)b * g.Hh + head) * g.N + j) * D;
-    if (MODE == kPair) {
-      out[fa] = __fdiv_rn(acc[0], n);
-      out[fb] = __fdiv_rn(acc[1 % NV], n);
-    } else {
+  if (POOL) {
+    // part[group][head][value][unit]: sums over the groups in order.
+    if (active) {
 #pragma unroll
-      for (int q = 0; q < NV / 4; ++q) {
-        if (q >= 2 && p0 < 0) break;
-        *reinterpret_cast<float4*>(out + (q < 2 ? fa : fb) + 4 * (q & 1)) =
-            make_float4(__fdiv_rn(acc[4 * q], n), __fdiv_rn(acc[4 * q + 1], n), __fdiv_rn(acc[4 * q + 2], n),
-                        __fdiv_rn(acc[4 * q + 3], n));
+      for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) part[((grp * kHeads + h) * NV + e) * P.nu + u] = acc[h][e];
+    }
+    __syncthreads();
+    const float n = (float)max(seen, 1);
+    const int per = NV * P.nu;
+    for (int o = tid; o < nh * per; o += kThreads) {
+      const int h = o / per, e = o % per / P.nu, v = o % P.nu;
+      float s = 0.f;
+      for (int k = 0; k < P.rg; ++k) s += part[(k * kHeads + h) * per + o % per];
+      int feat;
+      if (MODE == kInterleaved) {
+        feat = 8 * v + e;
+      } else if (MODE == kHalf8) {
+        if (8 * v >= R && e >= 8) continue;  // passed units have eight features
+        feat = 8 * v < R ? 8 * v + e + (e >= 8 ? R - 8 : 0) : R + 8 * v + e;
+      } else {
+        feat = v < R ? v + e * R : 2 * v + e;
       }
+      P.pooled[tensor][(((size_t)b * g.Hh + head0 + h) * g.N + j) * D + feat] = __fdiv_rn(s, n);
     }
   }
 }
@@ -265,14 +295,19 @@ rope_kernel(const __grid_constant__ RopeParams P) {
 template <int MODE>
 bsattn_status run(RopeParams& prm, int ntensor, bool pool, cudaStream_t st) {
   const Geom& g = prm.g;
-  const int nu = MODE == kInterleaved ? g.D / 8 : MODE == kHalf8 ? (g.D - prm.npairs) / 8 : g.D / 2;
-  prm.ncblk = (g.Hh * nu + kThreads - 1) / kThreads;
+  prm.nu = MODE == kInterleaved ? g.D / 8 : MODE == kHalf8 ? (g.D - prm.npairs) / 8 : g.D / 2;
+  prm.rg = kThreads / prm.nu;  // nu <= 64
+  prm.hblk = (g.Hh + kHeads - 1) / kHeads;
   prm.by_tile = pool ? 1 : 0;
-  const long long gx = pool ? g.N : (long long)g.N * g.nchunk;
-  if (g.B > 65535 || prm.ncblk * ntensor > 65535 || gx > 0x7fffffffLL) return BSATTN_ERR_UNSUPPORTED;
+  const long long gx = (pool ? g.N : (long long)g.N * g.nchunk) * prm.hblk;
+  if (g.B > 65535 || gx > 0x7fffffffLL) return BSATTN_ERR_UNSUPPORTED;
   const int box = g.ct > g.ch ? (g.ct > g.cw ? g.ct : g.cw) : (g.ch > g.cw ? g.ch : g.cw);
-  const size_t smem = (size_t)(prm.pos ? 64 : box) * prm.npairs * sizeof(float2);  // <= 32 KB
-  dim3 grid((unsigned)gx, g.B, prm.ncblk * ntensor);
+  const size_t smem = (size_t)(prm.pos ? g.cr : box) * prm.npairs * sizeof(float2);  // <= 32 KB
+  if (pool) {  // with the exchange buffer above the default 48 KB at the largest
+    if (cudaFuncSetAttribute(rope_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024) != cudaSuccess)
+      return BSATTN_ERR_CUDA;
+  }
+  dim3 grid((unsigned)gx, g.B, ntensor);
   if (pool)
     rope_kernel<MODE, true><<<grid, kThreads, smem, st>>>(prm);
   else
@@ -304,6 +339,14 @@ bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r) {
   return BSATTN_OK;
 }
 
+// x modulo 1 (x >= 0), in units of 2^-64.
+static unsigned long long fraction64(double x) {
+  x -= floor(x);
+  const double hi = floor(ldexp(x, 32));
+  const double lo = floor(ldexp(ldexp(x, 32) - hi, 32));
+  return ((unsigned long long)hi << 32) | (unsigned long long)lo;
+}
+
 bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv_bfloat16* x0, __nv_bfloat16* y0,
                           const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1, bool transpose,
                           const int32_t* doc, cudaStream_t st) {
@@ -331,7 +374,8 @@ bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv
           keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
           f *= keep + (1.0 - keep) / s;
         }
-        prm.turns[np++] = f / kTwoPi;
+        const double turn = f / kTwoPi;  // below 2^63 in any use; the fraction is exact in 2^-64
+        prm.turns[np++] = fraction64(turn);
       }
     }
   }
