@@ -127,6 +127,14 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   auto bar_sfull = [&](int b) { return sb + C::OFF_BAR + 8u * (1 + 2 * kStages + b); };
   auto bar_pfull = [&](int b) { return sb + C::OFF_BAR + 8u * (3 + 2 * kStages + b); };
   const uint32_t bar_final = sb + C::OFF_BAR + 8u * (5 + 2 * kStages);
+  // Score rules: one commit a step. The products that last read the stage of
+  // step m - kStages precede the S and dP products of step m - kStages + 2, so
+  // the stage is free when those are full. The wait starts with step 0's, two
+  // loads earlier than the ring needs it, so that every phase of the barrier
+  // is seen; none can be missed, because with at most four stages its next
+  // phase needs the load that waits here.
+  static_assert(!MOD || kStages <= 4, "the producer would miss a phase");
+  auto released = [](int m) { return m - kStages + 2; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* never = reinterpret_cast<volatile int*>(misc + 3);
@@ -246,7 +254,8 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       for (int s = 0; s < kStages; ++s) last[s] = -1;
       for (int m = 0; m < L; ++m) {
         const int s = m % kStages;
-        if (m >= kStages && !tc::mbar_wait(bar_empty(s), ((m / kStages) - 1) & 1, abort_flag, kWaitLimit)) {
+        if (m >= (MOD ? kStages - 2 : kStages) && !(MOD ? tc::mbar_wait(bar_sfull(released(m) & 1), (released(m) >> 1) & 1, abort_flag, kWaitLimit)
+                                  : tc::mbar_wait(bar_empty(s), ((m / kStages) - 1) & 1, abort_flag, kWaitLimit))) {
           *abort_flag = 1;
           atomicOr(P.err, BSATTN_DEVERR_TIMEOUT);
           break;
@@ -307,7 +316,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           tc::mma_ts_f16(tmem + kColDQ, dsA + acol, dk, idQ, acc);
           if (MOD) tc::mma_ts_f16(tmem + kColG, dsA + kColDP + acol, dk, idQ, acc);
         }
-        tc::mma_commit(bar_empty(s));
+        if (!MOD) tc::mma_commit(bar_empty(s));
         if (n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
@@ -664,6 +673,14 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   auto bar_sfull = [&](int b) { return sb + C::OFF_BAR + 8u * (1 + 2 * kStages + b); };
   auto bar_pfull = [&](int b) { return sb + C::OFF_BAR + 8u * (3 + 2 * kStages + b); };
   const uint32_t bar_final = sb + C::OFF_BAR + 8u * (5 + 2 * kStages);
+  // Score rules: one commit a step. The products that last read the stage of
+  // step m - kStages precede the S and dP products of step m - kStages + 2, so
+  // the stage is free when those are full. The wait starts with step 0's, two
+  // loads earlier than the ring needs it, so that every phase of the barrier
+  // is seen; none can be missed, because with at most four stages its next
+  // phase needs the load that waits here.
+  static_assert(!MOD || kStages <= 4, "the producer would miss a phase");
+  auto released = [](int m) { return m - kStages + 2; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* never = reinterpret_cast<volatile int*>(misc + 3);
@@ -782,7 +799,8 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       for (int s = 0; s < kStages; ++s) last[s] = -1;
       for (int m = 0; m < L; ++m) {
         const int s = m % kStages;
-        if (m >= kStages && !tc::mbar_wait(bar_empty(s), ((m / kStages) - 1) & 1, abort_flag, kWaitLimit)) {
+        if (m >= (MOD ? kStages - 2 : kStages) && !(MOD ? tc::mbar_wait(bar_sfull(released(m) & 1), (released(m) >> 1) & 1, abort_flag, kWaitLimit)
+                                  : tc::mbar_wait(bar_empty(s), ((m / kStages) - 1) & 1, abort_flag, kWaitLimit))) {
           *abort_flag = 1;
           atomicOr(P.err, BSATTN_DEVERR_TIMEOUT);
           break;
@@ -849,7 +867,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tc::mma_ts_f16(tmem + kColDK, dsA + acol, tc::smem_desc(st + kk * 2048, 8192, 1024, tc::kLayoutSW128),
                          idG, acc);
         }
-        tc::mma_commit(bar_empty(s));
+        if (!MOD) tc::mma_commit(bar_empty(s));
         if (n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
@@ -1101,9 +1119,9 @@ template <class C, class P>
 static size_t smem_of(const P& prm) {
   return 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
 }
-// Whether a deeper ring leaves room for the step lists. Under score rules the
-// ring holds four stages at D = 128 and six at D = 64: with three the step
-// time is the latency of a stage's loads, PLACEHOLDER.
+// Whether a fourth ring stage leaves room for the step lists. Under score
+// rules a stage is released by the S product two steps on, which leaves three
+// stages one step for a load's latency and four stages two.
 template <class C, class P>
 static bool fits(const P& prm) {
   return smem_of<C>(prm) <= 227 * 1024;
@@ -1139,7 +1157,7 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
     if (d128)
       return fits<DqCfg<128, true, 4>>(prm) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)
                                             : run_dq<128, true, 3>(p, q, k, v, d_o, prm, st);
-    return fits<DqCfg<64, true, 6>>(prm) ? run_dq<64, true, 6>(p, q, k, v, d_o, prm, st)
+    return fits<DqCfg<64, true, 4>>(prm) ? run_dq<64, true, 4>(p, q, k, v, d_o, prm, st)
                                          : run_dq<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
   return d128 ? run_dq<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dq<64, false, 3>(p, q, k, v, d_o, prm, st);
@@ -1172,7 +1190,7 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
     if (d128)
       return fits<KvCfg<128, true, 4>>(prm) ? run_dkdv<128, true, 4>(p, q, k, v, d_o, prm, st)
                                             : run_dkdv<128, true, 3>(p, q, k, v, d_o, prm, st);
-    return fits<KvCfg<64, true, 6>>(prm) ? run_dkdv<64, true, 6>(p, q, k, v, d_o, prm, st)
+    return fits<KvCfg<64, true, 4>>(prm) ? run_dkdv<64, true, 4>(p, q, k, v, d_o, prm, st)
                                          : run_dkdv<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
   return d128 ? run_dkdv<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dkdv<64, false, 3>(p, q, k, v, d_o, prm, st);

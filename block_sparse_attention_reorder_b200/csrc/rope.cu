@@ -65,7 +65,7 @@ constexpr int kHeads = 4;  // heads of a CTA
 constexpr uint32_t kHiddenRow = 1u << 31;
 
 template <int MODE, bool POOL>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, POOL ? (MODE == kHalf8 ? 3 : 4) : (MODE == kHalf8 ? 5 : 7))
 rope_kernel(const __grid_constant__ RopeParams P) {
   constexpr int NV = MODE == kPair ? 2 : MODE == kHalf8 ? 16 : 8;  // features of a unit
   constexpr int NP = NV / 2;

@@ -144,82 +144,105 @@ __device__ __forceinline__ int2 tile_ids(const Geom& g, const DocChunk* chunks, 
 // The rules on block scores, S' from S. Memory bound (8 bytes an entry): a
 // thread owns four neighbouring key tiles, whose mean coordinates and ranges
 // it keeps in registers (no division per entry), and walks kScoreRows query
-// tiles, whose own come from shared memory.
+// tiles, whose own come from shared memory, four rows' loads in flight.
+// PLACEHOLDER
 constexpr int kScoreRows = 32;
 constexpr int kScoreThreads = 128;
 
 struct TileMeta {
-  float t, h, w;  // mean coordinates of the real tokens
-  int first, last;  // frames
-  int2 ids;
+  float4 mean;  // mean (t, h, w) of the real tokens
+  int4 range;   // first and last frame, least and greatest id
 };
 __device__ __forceinline__ TileMeta tile_meta(const Geom& g, int j, int b, const DocChunk* ids) {
   const int t0 = j / (g.nH * g.nW) * g.tt, h0 = j / g.nW % g.nH * g.th, w0 = j % g.nW * g.tw;
   const int vt = min(g.tt, g.T - t0), vh = min(g.th, g.H - h0), vw = min(g.tw, g.W - w0);
-  TileMeta m{t0 + 0.5f * (vt - 1), h0 + 0.5f * (vh - 1), w0 + 0.5f * (vw - 1), t0, t0 + vt - 1, make_int2(0, 0)};
-  if (ids) m.ids = tile_ids(g, ids, b, j);
+  TileMeta m{make_float4(t0 + 0.5f * (vt - 1), h0 + 0.5f * (vh - 1), w0 + 0.5f * (vw - 1), 0.f),
+             make_int4(t0, t0 + vt - 1, 0, 0)};
+  if (ids) {
+    const int2 r = tile_ids(g, ids, b, j);
+    m.range.z = r.x;
+    m.range.w = r.y;
+  }
   return m;
 }
 
 template <bool VEC>
 __global__ void __launch_bounds__(kScoreThreads)
 mod_scores_kernel(Geom g, ModParams m, const float* S, float* out) {
-  __shared__ TileMeta rowm[kScoreRows];
+  __shared__ float4 row_mean[kScoreRows];
+  __shared__ int4 row_range[kScoreRows];
   const DocChunk* ids = m.doc_chunks;
   const int N = g.N, bh = blockIdx.z, b = bh / g.Hh, head = bh % g.Hh;
   const int i0 = blockIdx.y * kScoreRows, rows = min(kScoreRows, N - i0);
   const int j0 = 4 * (blockIdx.x * kScoreThreads + threadIdx.x);
-  if (threadIdx.x < rows) rowm[threadIdx.x] = tile_meta(g, i0 + threadIdx.x, b, ids);
+  if (threadIdx.x < rows) {
+    const TileMeta q = tile_meta(g, i0 + threadIdx.x, b, ids);
+    row_mean[threadIdx.x] = q.mean;
+    row_range[threadIdx.x] = q.range;
+  }
   __syncthreads();
   if (j0 >= N) return;
+  const int prefix = m.prefix ? __ldg(m.prefix + b) : 0;
   TileMeta km[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) km[e] = tile_meta(g, min(j0 + e, N - 1), b, ids);
+  for (int e = 0; e < 4; ++e) {
+    km[e] = tile_meta(g, min(j0 + e, N - 1), b, ids);
+    if (!m.causal || km[e].range.x < prefix) km[e].range.x = INT_MIN;  // never behind a query's last frame
+  }
   const float slope = m.slopes ? __ldg(m.slopes + head) : 0.f;
-  const int prefix = m.prefix ? __ldg(m.prefix + b) : 0;
   const float inv = m.cap > 0.f ? 1.f / m.cap : 0.f;
   const float* src = S + ((size_t)bh * N + i0) * N + j0;
   float* dst = out + ((size_t)bh * N + i0) * N + j0;
   const int ne = min(4, N - j0);
-#pragma unroll 4
-  for (int i = 0; i < rows; ++i) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (VEC) {
-      const float4 x = *reinterpret_cast<const float4*>(src + (size_t)i * N);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else {
+  constexpr int kBatch = 4;
+#pragma unroll 1
+  for (int ib = 0; ib < rows; ib += kBatch) {
+    float v[kBatch][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < ne) v[e] = src[(size_t)i * N + e];
-    }
-    const TileMeta q = rowm[i];
-    if (m.cap > 0.f) {
+    for (int x = 0; x < kBatch; ++x) {
+      const int i = min(ib + x, rows - 1);  // the last row again, not stored
+      if (VEC) {
+        const float4 y = *reinterpret_cast<const float4*>(src + (size_t)i * N);
+        v[x][0] = y.x; v[x][1] = y.y; v[x][2] = y.z; v[x][3] = y.w;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float2 u = make_float2(v[e] * inv, v[e + 1] * inv);
-        const float2 t = mod::tanh_small2(u);
-        v[e] = m.cap * (fabsf(u.x) <= mod::kSmall ? t.x : mod::tanh_any(u.x));
-        v[e + 1] = m.cap * (fabsf(u.y) <= mod::kSmall ? t.y : mod::tanh_any(u.y));
+        for (int e = 0; e < 4; ++e) v[x][e] = e < ne ? src[(size_t)i * N + e] : 0.f;
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int x = 0; x < kBatch; ++x) {
+      const int i = ib + x;
+      if (i >= rows) break;
+      if (m.cap > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float2 u = __fmul2_rn(make_float2(v[x][e], v[x][e + 1]), mod::bc(inv));
+          const float2 t = mod::tanh_small2(u);
+          v[x][e] = m.cap * (fabsf(u.x) <= mod::kSmall ? t.x : mod::tanh_any(u.x));
+          v[x][e + 1] = m.cap * (fabsf(u.y) <= mod::kSmall ? t.y : mod::tanh_any(u.y));
+        }
+      }
       if (m.slopes) {
-        float far = m.dist[0] * fabsf(q.t - km[e].t);
-        far = fmaf(m.dist[1], fabsf(q.h - km[e].h), far);
-        far = fmaf(m.dist[2], fabsf(q.w - km[e].w), far);
-        v[e] = fmaf(-slope, far, v[e]);
+        const float4 q = row_mean[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float far = m.dist[0] * fabsf(q.x - km[e].mean.x);
+          far = fmaf(m.dist[1], fabsf(q.y - km[e].mean.y), far);
+          far = fmaf(m.dist[2], fabsf(q.z - km[e].mean.z), far);
+          v[x][e] = fmaf(-slope, far, v[x][e]);
+        }
       }
-      bool hide = m.causal && km[e].first > q.last && km[e].first >= prefix;
-      if (ids) hide = hide || km[e].ids.x > q.ids.y || q.ids.x > km[e].ids.y;
-      if (hide) v[e] = -FLT_MAX;
-    }
-    if (VEC) {
-      *reinterpret_cast<float4*>(dst + (size_t)i * N) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+      const int4 q = row_range[i];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < ne) dst[(size_t)i * N + e] = v[e];
+        if (km[e].range.x > q.y || km[e].range.z > q.w || q.z > km[e].range.w) v[x][e] = -FLT_MAX;
+      if (VEC) {
+        *reinterpret_cast<float4*>(dst + (size_t)i * N) = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < ne) dst[(size_t)i * N + e] = v[x][e];
+      }
     }
   }
 }
