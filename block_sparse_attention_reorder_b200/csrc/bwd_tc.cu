@@ -60,8 +60,29 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColG = 384;
+constexpr uint32_t kColS = 0, kColDP = 128, kColOp = 192, kColDQ = 256, kColG = 384;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
+
+// Row r of a 128-row block in shared memory (128-byte swizzled 64-column
+// blocks of 16 KB) as an A operand in TMEM, two bf16 a column: the half that
+// `part` names, by the warps that own the row's lanes.
+template <int D>
+__device__ __forceinline__ bool operand_to_tmem(const uint8_t* block, uint32_t dst, int part, int r, uint32_t bar_loaded,
+                                                uint32_t bar_op, volatile int* abort_flag) {
+  if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_loaded, 0, abort_flag, kWaitLimit))) return false;
+  if (part < D / 64) {
+    uint32_t w[32];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(w + 4 * c) =
+          *reinterpret_cast<const uint4*>(block + part * 128 * 128 + r * 128 + ((c ^ (r & 7)) << 4));
+    tc::tmem_st32(dst + 32 * part, w);
+    tc::tmem_wait_st();
+  }
+  tc::fence_before_sync();
+  tc::mbar_arrive(bar_op);
+  return true;
+}
 
 struct DqParams {
   Geom g;
@@ -100,7 +121,7 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + kStages * T_BYTES;
   static constexpr int OFF_BAR = OFF_V + kStages * T_BYTES;
   // barriers: q, full[S], empty[S], sfull[2], pfull[2], final
-  static constexpr int NBAR = 1 + 2 * kStages + 5;
+  static constexpr int NBAR = 1 + 2 * kStages + 5 + (MOD ? 2 : 0);  // score rules: operand in TMEM, dP read
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort, L, zero
   static constexpr int OFF_COL = OFF_MISC + 16;        // 64 packed in-tile coordinates
   static constexpr int OFF_SCAN = OFF_COL + 256;
@@ -134,6 +155,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   // is seen; none can be missed, because with at most four stages its next
   // phase needs the load that waits here.
   static_assert(!MOD || kStages <= 4, "the producer would miss a phase");
+  const uint32_t bar_op = bar_final + 8, bar_ld = bar_final + 16;  // score rules only
   auto released = [](int m) { return m - kStages + 2; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -167,6 +189,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       tc::mbar_init(bar_pfull(x), kSoftmaxThreads);
     }
     tc::mbar_init(bar_final, 1);
+    if (MOD) {
+      tc::mbar_init(bar_op, kSoftmaxThreads);
+      tc::mbar_init(bar_ld, kSoftmaxThreads);
+    }
     misc[1] = 0;
     misc[3] = 0;
     tc::mbar_fence_init();
@@ -298,10 +324,42 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tc::mma_commit(bar_sfull(m & 1));
         return true;
       };
-      if (ok) ok = issue_sdp(0);
-      if (ok && L > 1) ok = issue_sdp(1);
+      // Score rules: S_m = Q K_m^T with Q from TMEM, and dP_m, whose one
+      // buffer is free once the softmax side has read dP_{m-1}.
+      auto issue_mod = [&](int m) -> bool {
+        const int s = m % kStages;
+        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < C::NKS; ++kk)
+          tc::mma_ts_f16(tmem + kColS + (m & 1) * 64, tmem + kColOp + kk * 8,
+                         tc::smem_desc(sb + C::OFF_K + s * C::T_BYTES + (kk / 4) * 64 * 128 + (kk % 4) * 32, 16, 1024,
+                                       tc::kLayoutSW128),
+                         idS, kk > 0 ? 1u : 0u);
+        if (m > 0 && !tc::mbar_wait(bar_ld, (m - 1) & 1, abort_flag, kWaitLimit)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < C::NKS; ++kk) {
+          const int cb = kk / 4, within = kk % 4;
+          tc::mma_ss_f16(tmem + kColDP, tc::smem_desc(sb + C::OFF_DO + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
+                         tc::smem_desc(sb + C::OFF_V + s * C::T_BYTES + cb * 64 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
+                         idS, kk > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(bar_sfull(m & 1));
+        return true;
+      };
+      if (MOD) {
+        ok = ok && tc::mbar_wait(bar_op, 0, abort_flag, kWaitLimit);
+        tc::fence_after_sync();
+      }
+      if (ok) ok = MOD ? issue_mod(0) : issue_sdp(0);
+      if (!MOD && ok && L > 1) ok = issue_sdp(1);
       for (int n = 0; ok && n < L; ++n) {
         const int s = n % kStages;
+        if (MOD && n + 1 < L && !issue_mod(n + 1)) {
+          ok = false;
+          break;
+        }
         if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit)) {
           ok = false;
           break;
@@ -314,10 +372,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const uint64_t dk = tc::smem_desc(sb + C::OFF_K + s * C::T_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
           const uint32_t acol = kk < 2 ? kk * 8 : 32 + (kk - 2) * 8, acc = (n > 0 || kk > 0) ? 1u : 0u;
           tc::mma_ts_f16(tmem + kColDQ, dsA + acol, dk, idQ, acc);
-          if (MOD) tc::mma_ts_f16(tmem + kColG, dsA + kColDP + acol, dk, idQ, acc);
+          if (MOD) tc::mma_ts_f16(tmem + kColG, dsA + 16 + acol, dk, idQ, acc);
         }
         if (!MOD) tc::mma_commit(bar_empty(s));
-        if (n + 2 < L && !issue_sdp(n + 2)) {
+        if (!MOD && n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
         }
@@ -342,6 +400,9 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const float dlt = row_exists ? P.delta[lrow] : 0.f;
     const float c = P.scale_log2;
     bool ok = true;
+    if constexpr (MOD) {
+      if (L > 0) ok = operand_to_tmem<D>(smem + C::OFF_Q, tmem + lane_base + kColOp, part, r, bar_q, bar_op, abort_flag);
+    }
     mod::Row row{};
     float kc = 0.f;  // takes raw scores to the argument of tanh
     float slope = 0.f;
@@ -365,7 +426,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       tc::fence_after_sync();
       const uint32_t sbuf = tmem + lane_base + kColS + (n & 1) * 64 + 32 * part;
-      const uint32_t pbuf = tmem + lane_base + kColDP + (n & 1) * 64 + 32 * part;
+      const uint32_t pbuf = tmem + lane_base + kColDP + (MOD ? 0 : (n & 1) * 64) + 32 * part;
       uint32_t dsw[16];
       uint32_t gw[MOD ? 16 : 1];  // P (1 - tanh^2)
       if constexpr (MOD) {
@@ -393,6 +454,8 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
+          tc::fence_before_sync();
+          tc::mbar_arrive(bar_ld);
           // log2 of P = raw scores (or tanh values) times c2, bias, minus the log-sum-exp.
           float c2 = c;
           if (M.cap > 0.f) {
@@ -467,9 +530,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if constexpr (MOD) {
 #pragma unroll
           for (int q = 0; q < 16; ++q) gw[q] = 0u;
+          tc::mbar_arrive(bar_ld);
         }
       }
-      if constexpr (MOD) tc::tmem_st16(pbuf, gw);
+      if constexpr (MOD) tc::tmem_st16(sbuf + 16, gw);  // P (1 - tanh^2) over the second 16
       tc::tmem_st16(sbuf, dsw);  // dS of this half over the first 16 columns of its S
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -644,7 +708,8 @@ struct KvCfg {
   static constexpr int OFF_V = OFF_K + BLK_BYTES;
   static constexpr int OFF_RING = OFF_V + BLK_BYTES;
   static constexpr int OFF_BAR = OFF_RING + kStages * STAGE;
-  static constexpr int NBAR = 1 + 2 * kStages + 5;  // kv, full[S], empty[S], sfull[2], pfull[2], final
+  // kv, full[S], empty[S], sfull[2], pfull[2], final; score rules: operand in TMEM, dP read
+  static constexpr int NBAR = 1 + 2 * kStages + 5 + (MOD ? 2 : 0);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_COL = OFF_MISC + 16;
   static constexpr int OFF_SCAN = OFF_COL + 256;
@@ -662,7 +727,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ std::conditional_t<MOD, KvParamsMod, KvParams> P) {
   using C = KvCfg<D, MOD, kStages>;
-  constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 256 + D;
+  constexpr uint32_t kColST = 0, kColDPT = 128, kColOp = 192, kColDV = 256, kColDK = 256 + D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -680,6 +745,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // is seen; none can be missed, because with at most four stages its next
   // phase needs the load that waits here.
   static_assert(!MOD || kStages <= 4, "the producer would miss a phase");
+  const uint32_t bar_op = bar_final + 8, bar_ld = bar_final + 16;  // score rules only
   auto released = [](int m) { return m - kStages + 2; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -721,6 +787,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tc::mbar_init(bar_pfull(x), kSoftmaxThreads);
     }
     tc::mbar_init(bar_final, 1);
+    if (MOD) {
+      tc::mbar_init(bar_op, kSoftmaxThreads);
+      tc::mbar_init(bar_ld, kSoftmaxThreads);
+    }
     misc[1] = 0;
     misc[3] = 0;
     tc::mbar_fence_init();
@@ -846,10 +916,42 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         tc::mma_commit(bar_sfull(m & 1));
         return true;
       };
-      if (ok) ok = issue_sdp(0);
-      if (ok && L > 1) ok = issue_sdp(1);
+      // Score rules: S^T_m = K Q_m^T with K from TMEM, and dP^T_m, whose one
+      // buffer is free once the softmax side has read dP^T_{m-1}.
+      auto issue_mod = [&](int m) -> bool {
+        const int s = m % kStages;
+        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        tc::fence_after_sync();
+        const uint32_t st = sb + C::OFF_RING + s * C::STAGE;
+#pragma unroll
+        for (int kk = 0; kk < C::NKS; ++kk)
+          tc::mma_ts_f16(tmem + kColST + (m & 1) * 64, tmem + kColOp + kk * 8,
+                         tc::smem_desc(st + (kk / 4) * 64 * 128 + (kk % 4) * 32, 16, 1024, tc::kLayoutSW128), idS,
+                         kk > 0 ? 1u : 0u);
+        if (m > 0 && !tc::mbar_wait(bar_ld, (m - 1) & 1, abort_flag, kWaitLimit)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < C::NKS; ++kk) {
+          const int cb = kk / 4, within = kk % 4;
+          tc::mma_ss_f16(tmem + kColDPT, tc::smem_desc(sb + C::OFF_V + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
+                         tc::smem_desc(st + C::T_BYTES + cb * 64 * 128 + within * 32, 16, 1024, tc::kLayoutSW128), idS,
+                         kk > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(bar_sfull(m & 1));
+        return true;
+      };
+      if (MOD) {
+        ok = ok && tc::mbar_wait(bar_op, 0, abort_flag, kWaitLimit);
+        tc::fence_after_sync();
+      }
+      if (ok) ok = MOD ? issue_mod(0) : issue_sdp(0);
+      if (!MOD && ok && L > 1) ok = issue_sdp(1);
       for (int n = 0; ok && n < L; ++n) {
         const int s = n % kStages;
+        if (MOD && n + 1 < L && !issue_mod(n + 1)) {
+          ok = false;
+          break;
+        }
         if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit)) {
           ok = false;
           break;
@@ -857,7 +959,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         tc::fence_after_sync();
         const uint32_t st = sb + C::OFF_RING + s * C::STAGE;
         // P^T and dS^T (bf16): queries 0-31 in columns 0-15, 32-63 in 32-47.
-        const uint32_t pA = tmem + kColST + (n & 1) * 64, dsA = tmem + kColDPT + (n & 1) * 64;
+        const uint32_t pA = tmem + kColST + (n & 1) * 64, dsA = MOD ? pA + 16 : tmem + kColDPT + (n & 1) * 64;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // 16 queries per MMA: 2048 bytes of the dO / Q tile
           const uint32_t acol = kk < 2 ? kk * 8 : 32 + (kk - 2) * 8;
@@ -868,7 +970,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                          idG, acc);
         }
         if (!MOD) tc::mma_commit(bar_empty(s));
-        if (n + 2 < L && !issue_sdp(n + 2)) {
+        if (!MOD && n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
         }
@@ -891,6 +993,9 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float c = P.scale_log2;
     bool ok = true;
+    if constexpr (MOD) {
+      if (L > 0) ok = operand_to_tmem<D>(smem + C::OFF_K, tmem + lane_base + kColOp, part, r, bar_kv, bar_op, abort_flag);
+    }
     mod::Row row{};
     float kc = 0.f;  // takes raw scores to the argument of tanh
     float slope = 0.f;
@@ -908,7 +1013,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       tc::fence_after_sync();
       const uint32_t sbuf = tmem + lane_base + kColST + (n & 1) * 64 + 32 * part;
-      const uint32_t pbuf = tmem + lane_base + kColDPT + (n & 1) * 64 + 32 * part;
+      const uint32_t pbuf = tmem + lane_base + kColDPT + (MOD ? 0 : (n & 1) * 64) + 32 * part;
       // lse and Delta of this step's query tile came with its TMA copies:
       // observe their barrier before reading them.
       if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_full(n % kStages), (n / kStages) & 1, abort_flag, kWaitLimit))) {
@@ -945,6 +1050,8 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
+          tc::fence_before_sync();
+          tc::mbar_arrive(bar_ld);
           float c2 = c;
           if (M.cap > 0.f) {
             c2 = M.cap * mod::kLog2e;
@@ -1012,9 +1119,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q) pw[q] = dw[q] = 0u;
+        if (MOD) tc::mbar_arrive(bar_ld);
       }
       tc::tmem_st16(sbuf, pw);  // P^T over the first 16 columns of this half of S^T
-      tc::tmem_st16(pbuf, dw);  // dS^T over the first 16 columns of this half of dP^T
+      // dS^T over the first 16 columns of this half of dP^T; with rules over the
+      // second 16 of S^T, so that dP^T is free as soon as it is read.
+      tc::tmem_st16(MOD ? sbuf + 16 : pbuf, dw);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       tc::mbar_arrive(bar_pfull(n & 1));
