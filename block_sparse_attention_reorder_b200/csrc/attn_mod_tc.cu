@@ -155,7 +155,8 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const bool has1 = i1 >= 0;
   // First tiled-layout row of chunk c of tile j.
   auto tiled_row = [&](int j, int c) -> int { return (int)((bh * g.N + j) * g.V) + 64 * c; };
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be uniform
 
   // The list counts and this thread's first entry of each list come first, so
   // that their latency overlaps the set-up (entries at and beyond a count are
@@ -242,8 +243,8 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = misc[0];
-  const int L = (int)misc[2];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 4) {
@@ -328,16 +329,20 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   } else if (warp == 5) {
-    if (lane == 0 && L > 0) {
+    if (L > 0) {
+      const uint32_t lead = tc::elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, P.wait_limit));
+      };
       constexpr uint32_t idS = FP8 ? tc::instr_desc(0, 0, 0, 0, 64, 128) : tc::instr_desc(1, 1, 0, 0, 64, 128);
       constexpr uint32_t idPV = tc::instr_desc(1, 1, 0, 1, D, 128);
       // Testing hook: bar_final gets its first arrival only from the final
       // commit below, so this wait runs out and the CTA takes the timeout path.
-      bool ok = !P.stall || tc::mbar_wait(bar_final, 0, abort_flag, P.wait_limit);
-      ok = ok && tc::mbar_wait(bar_q, 0, abort_flag, P.wait_limit);
+      bool ok = !P.stall || wait(bar_final, 0);
+      ok = ok && wait(bar_q, 0);
       auto issue_S = [&](int m) -> bool {
         const int s = m % kStages;
-        if (!tc::mbar_wait(bar_kfull(s), (m / kStages) & 1, abort_flag, P.wait_limit)) return false;
+        if (!wait(bar_kfull(s), (m / kStages) & 1)) return false;
         tc::fence_after_sync();
         const uint32_t dS = tmem + ((m & 1) ? kColS1 : kColS0);
 #pragma unroll
@@ -347,19 +352,18 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           const uint64_t db =
               tc::smem_desc(sb + C::OFF_K + s * C::K_BYTES + cb * 64 * C::SWB + within * 32, 16, 8 * C::SWB, C::LAYOUT);
           if (FP8)
-            tc::mma_ss_f8(dS, da, db, idS, kk > 0 ? 1u : 0u);
+            tc::mma_ss_f8_warp(lead, dS, da, db, idS, kk > 0 ? 1u : 0u);
           else
-            tc::mma_ss_f16(dS, da, db, idS, kk > 0 ? 1u : 0u);
+            tc::mma_ss_f16_warp(lead, dS, da, db, idS, kk > 0 ? 1u : 0u);
         }
-        tc::mma_commit(bar_sfull(m & 1));
+        tc::mma_commit_warp(lead, bar_sfull(m & 1));
         return true;
       };
       if (ok) ok = issue_S(0);
       if (ok && L > 1) ok = issue_S(1);
       for (int n = 0; ok && n < L; ++n) {
         const int s = n % kStages;
-        if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, P.wait_limit) ||
-            !tc::mbar_wait(bar_vfull(s), (n / kStages) & 1, abort_flag, P.wait_limit)) {
+        if (!wait(bar_pfull(n & 1), (n >> 1) & 1) || !wait(bar_vfull(s), (n / kStages) & 1)) {
           ok = false;
           break;
         }
@@ -368,17 +372,17 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t dv = tc::smem_desc(sb + C::OFF_V + s * C::V_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
-          tc::mma_ts_f16(tmem + kColO, pA + (kSplit && kk >= 2 ? 16 : 0) + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_ts_f16_warp(lead, tmem + kColO, pA + (kSplit && kk >= 2 ? 16 : 0) + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
         }
-        tc::mma_commit(bar_pvdone(n & 1));
+        tc::mma_commit_warp(lead, bar_pvdone(n & 1));
         if (n + 2 < L && !issue_S(n + 2)) {
           ok = false;
           break;
         }
       }
-      if (!ok) record_timeout(abort_flag, P.err);
+      if (!ok && lead) record_timeout(abort_flag, P.err);
       // Every MMA issued so far has finished before TMEM is released.
-      tc::mma_commit(bar_final);
+      tc::mma_commit_warp(lead, bar_final);
       tc::mbar_wait(bar_final, 0, never, kWaitLimit);
     }
     __syncwarp();
