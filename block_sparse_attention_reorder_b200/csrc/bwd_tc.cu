@@ -173,7 +173,8 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int head = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * g.Hh + head;
   const bool has1 = i1 >= 0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be uniform
   // First tiled-layout row of chunk c of tile j.
   auto tile_row = [&](int j, int c) -> int { return (int)((bh * g.N + j) * g.V) + 64 * c; };
 
@@ -255,8 +256,8 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = misc[0];
-  const int L = (int)misc[2];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {
@@ -302,54 +303,58 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
   } else if (warp == 9) {
-    if (lane == 0 && L > 0) {
+    if (L > 0) {
+      const uint32_t lead = tc::elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, kWaitLimit));
+      };
       constexpr uint32_t idS = tc::instr_desc(1, 1, 0, 0, 64, 128);   // bf16, K-major A and B, N = 64
       constexpr uint32_t idQ = tc::instr_desc(1, 1, 0, 1, D, 128);    // B (K tile) MN-major, N = D
-      bool ok = tc::mbar_wait(bar_q, 0, abort_flag, kWaitLimit);
+      bool ok = wait(bar_q, 0);
       // S_m = Q K_m^T and dP_m = dO V_m^T into buffer m & 1.
       auto issue_sdp = [&](int m) -> bool {
         const int s = m % kStages;
-        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        if (!wait(bar_full(s), (m / kStages) & 1)) return false;
         tc::fence_after_sync();
         const uint32_t dS = tmem + kColS + (m & 1) * 64, dP = tmem + kColDP + (m & 1) * 64;
 #pragma unroll
         for (int kk = 0; kk < C::NKS; ++kk) {
           const int cb = kk / 4, within = kk % 4;
           const uint32_t aoff = cb * 128 * 128 + within * 32, boff = s * C::T_BYTES + cb * 64 * 128 + within * 32;
-          tc::mma_ss_f16(dS, tc::smem_desc(sb + C::OFF_Q + aoff, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, dS, tc::smem_desc(sb + C::OFF_Q + aoff, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(sb + C::OFF_K + boff, 16, 1024, tc::kLayoutSW128), idS, kk > 0 ? 1u : 0u);
-          tc::mma_ss_f16(dP, tc::smem_desc(sb + C::OFF_DO + aoff, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, dP, tc::smem_desc(sb + C::OFF_DO + aoff, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(sb + C::OFF_V + boff, 16, 1024, tc::kLayoutSW128), idS, kk > 0 ? 1u : 0u);
         }
-        tc::mma_commit(bar_sfull(m & 1));
+        tc::mma_commit_warp(lead, bar_sfull(m & 1));
         return true;
       };
       // Score rules: S_m = Q K_m^T with Q from TMEM, and dP_m, whose one
       // buffer is free once the softmax side has read dP_{m-1}.
       auto issue_mod = [&](int m) -> bool {
         const int s = m % kStages;
-        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        if (!wait(bar_full(s), (m / kStages) & 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < C::NKS; ++kk)
-          tc::mma_ts_f16(tmem + kColS + (m & 1) * 64, tmem + kColOp + kk * 8,
+          tc::mma_ts_f16_warp(lead, tmem + kColS + (m & 1) * 64, tmem + kColOp + kk * 8,
                          tc::smem_desc(sb + C::OFF_K + s * C::T_BYTES + (kk / 4) * 64 * 128 + (kk % 4) * 32, 16, 1024,
                                        tc::kLayoutSW128),
                          idS, kk > 0 ? 1u : 0u);
-        if (m > 0 && !tc::mbar_wait(bar_ld, (m - 1) & 1, abort_flag, kWaitLimit)) return false;
+        if (m > 0 && !wait(bar_ld, (m - 1) & 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < C::NKS; ++kk) {
           const int cb = kk / 4, within = kk % 4;
-          tc::mma_ss_f16(tmem + kColDP, tc::smem_desc(sb + C::OFF_DO + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, tmem + kColDP, tc::smem_desc(sb + C::OFF_DO + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(sb + C::OFF_V + s * C::T_BYTES + cb * 64 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
                          idS, kk > 0 ? 1u : 0u);
         }
-        tc::mma_commit(bar_sfull(m & 1));
+        tc::mma_commit_warp(lead, bar_sfull(m & 1));
         return true;
       };
       if (MOD) {
-        ok = ok && tc::mbar_wait(bar_op, 0, abort_flag, kWaitLimit);
+        ok = ok && wait(bar_op, 0);
         tc::fence_after_sync();
       }
       if (ok) ok = MOD ? issue_mod(0) : issue_sdp(0);
@@ -360,7 +365,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ok = false;
           break;
         }
-        if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit)) {
+        if (!wait(bar_pfull(n & 1), (n >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -371,20 +376,20 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int kk = 0; kk < 4; ++kk) {  // 16 keys per MMA: 2048 bytes of the K tile
           const uint64_t dk = tc::smem_desc(sb + C::OFF_K + s * C::T_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
           const uint32_t acol = kk < 2 ? kk * 8 : 32 + (kk - 2) * 8, acc = (n > 0 || kk > 0) ? 1u : 0u;
-          tc::mma_ts_f16(tmem + kColDQ, dsA + acol, dk, idQ, acc);
-          if (MOD) tc::mma_ts_f16(tmem + kColG, dsA + 16 + acol, dk, idQ, acc);
+          tc::mma_ts_f16_warp(lead, tmem + kColDQ, dsA + acol, dk, idQ, acc);
+          if (MOD) tc::mma_ts_f16_warp(lead, tmem + kColG, dsA + 16 + acol, dk, idQ, acc);
         }
-        if (!MOD) tc::mma_commit(bar_empty(s));
+        if (!MOD) tc::mma_commit_warp(lead, bar_empty(s));
         if (!MOD && n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
         }
       }
-      if (!ok) {
+      if (!ok && lead) {
         *abort_flag = 1;
         atomicOr(P.err, BSATTN_DEVERR_TIMEOUT);
       }
-      tc::mma_commit(bar_final);
+      tc::mma_commit_warp(lead, bar_final);
       tc::mbar_wait(bar_final, 0, never, kWaitLimit);
     }
     __syncwarp();
@@ -763,7 +768,8 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const int head = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * g.Hh + head;
   const bool has1 = j1 >= 0;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be uniform
   // First tiled-layout row of chunk c of tile j.
   auto tile_row = [&](int j, int c) -> int { return (int)((bh * g.N + j) * g.V) + 64 * c; };
   // Whether row q of chunk c of tile j is a real token.
@@ -844,8 +850,8 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = misc[0];
-  const int L = (int)misc[2];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {
@@ -894,13 +900,17 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   } else if (warp == 9) {
-    if (lane == 0 && L > 0) {
+    if (L > 0) {
+      const uint32_t lead = tc::elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, kWaitLimit));
+      };
       constexpr uint32_t idS = tc::instr_desc(1, 1, 0, 0, 64, 128);  // K-major A and B, N = 64
       constexpr uint32_t idG = tc::instr_desc(1, 1, 0, 1, D, 128);   // B MN-major, N = D
-      bool ok = tc::mbar_wait(bar_kv, 0, abort_flag, kWaitLimit);
+      bool ok = wait(bar_kv, 0);
       auto issue_sdp = [&](int m) -> bool {
         const int s = m % kStages;
-        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        if (!wait(bar_full(s), (m / kStages) & 1)) return false;
         tc::fence_after_sync();
         const uint32_t st = sb + C::OFF_RING + s * C::STAGE;
         const uint32_t dS = tmem + kColST + (m & 1) * 64, dP = tmem + kColDPT + (m & 1) * 64;
@@ -908,40 +918,40 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int kk = 0; kk < C::NKS; ++kk) {
           const int cb = kk / 4, within = kk % 4;
           const uint32_t aoff = cb * 128 * 128 + within * 32, boff = cb * 64 * 128 + within * 32;
-          tc::mma_ss_f16(dS, tc::smem_desc(sb + C::OFF_K + aoff, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, dS, tc::smem_desc(sb + C::OFF_K + aoff, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(st + boff, 16, 1024, tc::kLayoutSW128), idS, kk > 0 ? 1u : 0u);
-          tc::mma_ss_f16(dP, tc::smem_desc(sb + C::OFF_V + aoff, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, dP, tc::smem_desc(sb + C::OFF_V + aoff, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(st + C::T_BYTES + boff, 16, 1024, tc::kLayoutSW128), idS, kk > 0 ? 1u : 0u);
         }
-        tc::mma_commit(bar_sfull(m & 1));
+        tc::mma_commit_warp(lead, bar_sfull(m & 1));
         return true;
       };
       // Score rules: S^T_m = K Q_m^T with K from TMEM, and dP^T_m, whose one
       // buffer is free once the softmax side has read dP^T_{m-1}.
       auto issue_mod = [&](int m) -> bool {
         const int s = m % kStages;
-        if (!tc::mbar_wait(bar_full(s), (m / kStages) & 1, abort_flag, kWaitLimit)) return false;
+        if (!wait(bar_full(s), (m / kStages) & 1)) return false;
         tc::fence_after_sync();
         const uint32_t st = sb + C::OFF_RING + s * C::STAGE;
 #pragma unroll
         for (int kk = 0; kk < C::NKS; ++kk)
-          tc::mma_ts_f16(tmem + kColST + (m & 1) * 64, tmem + kColOp + kk * 8,
+          tc::mma_ts_f16_warp(lead, tmem + kColST + (m & 1) * 64, tmem + kColOp + kk * 8,
                          tc::smem_desc(st + (kk / 4) * 64 * 128 + (kk % 4) * 32, 16, 1024, tc::kLayoutSW128), idS,
                          kk > 0 ? 1u : 0u);
-        if (m > 0 && !tc::mbar_wait(bar_ld, (m - 1) & 1, abort_flag, kWaitLimit)) return false;
+        if (m > 0 && !wait(bar_ld, (m - 1) & 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < C::NKS; ++kk) {
           const int cb = kk / 4, within = kk % 4;
-          tc::mma_ss_f16(tmem + kColDPT, tc::smem_desc(sb + C::OFF_V + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
+          tc::mma_ss_f16_warp(lead, tmem + kColDPT, tc::smem_desc(sb + C::OFF_V + cb * 128 * 128 + within * 32, 16, 1024, tc::kLayoutSW128),
                          tc::smem_desc(st + C::T_BYTES + cb * 64 * 128 + within * 32, 16, 1024, tc::kLayoutSW128), idS,
                          kk > 0 ? 1u : 0u);
         }
-        tc::mma_commit(bar_sfull(m & 1));
+        tc::mma_commit_warp(lead, bar_sfull(m & 1));
         return true;
       };
       if (MOD) {
-        ok = ok && tc::mbar_wait(bar_op, 0, abort_flag, kWaitLimit);
+        ok = ok && wait(bar_op, 0);
         tc::fence_after_sync();
       }
       if (ok) ok = MOD ? issue_mod(0) : issue_sdp(0);
@@ -952,7 +962,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           ok = false;
           break;
         }
-        if (!tc::mbar_wait(bar_pfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit)) {
+        if (!wait(bar_pfull(n & 1), (n >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -964,22 +974,22 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int kk = 0; kk < 4; ++kk) {  // 16 queries per MMA: 2048 bytes of the dO / Q tile
           const uint32_t acol = kk < 2 ? kk * 8 : 32 + (kk - 2) * 8;
           const uint32_t acc = (n > 0 || kk > 0) ? 1u : 0u;
-          tc::mma_ts_f16(tmem + kColDV, pA + acol,
+          tc::mma_ts_f16_warp(lead, tmem + kColDV, pA + acol,
                          tc::smem_desc(st + C::T_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128), idG, acc);
-          tc::mma_ts_f16(tmem + kColDK, dsA + acol, tc::smem_desc(st + kk * 2048, 8192, 1024, tc::kLayoutSW128),
+          tc::mma_ts_f16_warp(lead, tmem + kColDK, dsA + acol, tc::smem_desc(st + kk * 2048, 8192, 1024, tc::kLayoutSW128),
                          idG, acc);
         }
-        if (!MOD) tc::mma_commit(bar_empty(s));
+        if (!MOD) tc::mma_commit_warp(lead, bar_empty(s));
         if (!MOD && n + 2 < L && !issue_sdp(n + 2)) {
           ok = false;
           break;
         }
       }
-      if (!ok) {
+      if (!ok && lead) {
         *abort_flag = 1;
         atomicOr(P.err, BSATTN_DEVERR_TIMEOUT);
       }
-      tc::mma_commit(bar_final);
+      tc::mma_commit_warp(lead, bar_final);
       tc::mbar_wait(bar_final, 0, never, kWaitLimit);
     }
     __syncwarp();
