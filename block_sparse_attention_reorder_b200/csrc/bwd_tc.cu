@@ -423,7 +423,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (P.mod.cap > 0.f) kc = P.scale / P.mod.cap;
     }
     for (int n = 0; n < L; ++n) {
-      const uint32_t e = ulist[n];
+      const uint32_t e = ulist[n], ext = uext[n];
       const bool keep = row_exists && ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
       if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_sfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit))) {
         ok = false;
@@ -435,7 +435,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       uint32_t dsw[16];
       uint32_t gw[MOD ? 16 : 1];  // P (1 - tanh^2)
       if constexpr (MOD) {
-        if ((uext[n] & mod::kHidden) && tid < 64) {  // K rows of hidden tokens (S has been formed)
+        if ((ext & mod::kHidden) && tid < 64) {  // K rows of hidden tokens (S has been formed)
           const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
           if (__ldg(P.mod.doc_rows + first + tid) < 0)
             mod::zero_row(smem + C::OFF_K + (n % kStages) * C::T_BYTES, C::QBLK, tid);
@@ -445,17 +445,19 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (MOD && keep) {
         if constexpr (MOD) {
           const ModParams& M = P.mod;
-          const uint32_t ext = uext[n];
-          const ChunkOrigin org = tab->at((int)((e >> 21) & 0x1FFu));
-          const mod::Coord f = mod::chunk_first(g, M, ext, org);
-          uint32_t vis = row.live ? 0xffffffffu : 0u;
-          if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
+          // (Rows without a token need no mask: P is 0 through neg_lse2 there.)
+          mod::Coord f{};
+          uint32_t vis = 0xffffffffu;
+          bool partial = false;
+          if (M.slopes || (ext & mod::kSpecial)) f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
+          if (ext & mod::kSpecial) {
             int vt = g.T - f.t;
             if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
             unsigned long long all = mod::visible_box(g, &tab->col, 0, vt, g.H - f.h, g.W - f.w);
             if (ext & mod::kDoc)
               all &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.nchunk + ((e >> 21) & 0x1FFu), row.id);
             vis = (uint32_t)(all >> (32 * part));
+            partial = __any_sync(0xffffffffu, vis != 0xffffffffu);
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
@@ -465,14 +467,12 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           float c2 = c;
           if (M.cap > 0.f) {
             c2 = M.cap * mod::kLog2e;
-            if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) mod::set_unseen<32>(sr, vis, 0.f);
+            if (partial) mod::set_unseen<32>(sr, vis, 0.f);
             mod::tanh_scores<32>(sr, kc);
           }
           float far[32];
           if (M.slopes) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) far[q] = 0.f;
-            mod::add_distance<32>(g, far, &tab->col, 32 * part, mod::make_dist(g, M, row.at, f, 1.f));
+            mod::add_distance<32, true>(g, far, &tab->col, 32 * part, mod::make_dist(g, M, row.at, f, 1.f));
           }
           const float2 cc2 = mod::bc(c2), ss2 = mod::bc(-slope * mod::kLog2e), nl2 = mod::bc(nlse2), nd2 = mod::bc(ndlt);
           auto form = [&](auto masked, auto cap, auto bias) {
@@ -504,10 +504,9 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               gw[q] = mod::pack(p);
             }
           };
-          mod::dispatch(!__all_sync(0xffffffffu, vis == 0xffffffffu), M.cap > 0.f, M.slopes != nullptr, form);
+          mod::dispatch(partial, M.cap > 0.f, M.slopes != nullptr, form);
         }
       } else if (!MOD && keep) {
-        const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
         const int vt = (int)(ext & 0xffu), vh = (int)((ext >> 8) & 0xffu), vw = (int)((ext >> 16) & 0xffu);
         uint32_t sr[32], pr[32];
@@ -1015,7 +1014,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (P.mod.cap > 0.f) kc = P.scale / P.mod.cap;
     }
     for (int n = 0; n < L; ++n) {
-      const uint32_t e = ulist[n];
+      const uint32_t e = ulist[n], ext = uext[n];
       const bool keep = row_exists && ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
       if (!__all_sync(0xffffffffu, tc::mbar_wait(bar_sfull(n & 1), (n >> 1) & 1, abort_flag, kWaitLimit))) {
         ok = false;
@@ -1032,7 +1031,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       uint32_t pw[16], dw[16];
       if constexpr (MOD) {
-        if ((uext[n] & mod::kHidden) && tid < 64) {  // Q and dO rows of hidden tokens (S and dP have been formed)
+        if ((ext & mod::kHidden) && tid < 64) {  // Q and dO rows of hidden tokens (S and dP have been formed)
           const size_t first = ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.V + 64 * ((e >> 21) & 0x1FFu);
           if (__ldg(P.mod.doc_rows + first + tid) < 0) {
             uint8_t* tile = smem + C::OFF_RING + (n % kStages) * C::STAGE;
@@ -1046,17 +1045,19 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if constexpr (MOD) {
           const ModParams& M = P.mod;
           const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
-          const uint32_t ext = uext[n];
-          const ChunkOrigin org = tab->at((int)((e >> 21) & 0x1FFu));
-          const mod::Coord f = mod::chunk_first(g, M, ext, org);
-          uint32_t vis = row.live ? 0xffffffffu : 0u;
-          if (row.live && (ext & (mod::kEdge | mod::kCausal | mod::kDoc))) {
+          // (Rows without a token need no mask: their gradients are not written.)
+          mod::Coord f{};
+          uint32_t vis = 0xffffffffu;
+          bool partial = false;
+          if (M.slopes || (ext & mod::kSpecial)) f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
+          if (ext & mod::kSpecial) {
             // Queries at or behind the key's frame, all of them for a key of the prefix.
             const int lo = M.causal && row.at.t >= prefix ? row.at.t - f.t : 0;
             unsigned long long all = mod::visible_box(g, &tab->col, lo, g.T - f.t, g.H - f.h, g.W - f.w);
             if (ext & mod::kDoc)
               all &= mod::visible_doc(M, ((size_t)b * g.N + (e & 0x1FFFFFu)) * g.nchunk + ((e >> 21) & 0x1FFu), row.id);
             vis = (uint32_t)(all >> (32 * part));
+            partial = __any_sync(0xffffffffu, vis != 0xffffffffu);
           }
           uint32_t sr[32], pr[32];
           tc::tmem_ld32x2_wait(sbuf, sr, pbuf, pr);
@@ -1065,7 +1066,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           float c2 = c;
           if (M.cap > 0.f) {
             c2 = M.cap * mod::kLog2e;
-            if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) mod::set_unseen<32>(sr, vis, 0.f);
+            if (partial) mod::set_unseen<32>(sr, vis, 0.f);
             mod::tanh_scores<32>(sr, kc);
           }
           float y[32];  // -lse log2(e) of the queries, plus the bias
@@ -1097,11 +1098,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               }
             }
           };
-          mod::dispatch(!__all_sync(0xffffffffu, vis == 0xffffffffu), M.cap > 0.f, false, form);
+          mod::dispatch(partial, M.cap > 0.f, false, form);
         }
       } else if (!MOD && keep) {
         const float* ld = reinterpret_cast<const float*>(smem + C::OFF_RING + (n % kStages) * C::STAGE + 2 * C::T_BYTES);
-        const uint32_t ext = uext[n];
         const bool edge = (ext >> 31) != 0;
         const int vt = (int)(ext & 0xffu), vh = (int)((ext >> 8) & 0xffu), vw = (int)((ext >> 16) & 0xffu);
         uint32_t sr[32], pr[32];

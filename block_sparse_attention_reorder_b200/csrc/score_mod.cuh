@@ -299,7 +299,7 @@ __device__ __forceinline__ unsigned long long visible_doc(const ModParams& m, si
 
 // Distance bias of a token at offset (t, h, w) from the chunk's first token,
 // weights nt, nh, nw (0 for an axis of one token): y[q] += sum of weight times
-// |offset - the row's|; with y = 0 and positive weights the distance itself.
+// |offset - the row's|; with SET and positive weights y becomes the distance.
 struct Dist {
   float t, h, w, nt, nh, nw;
 };
@@ -308,10 +308,14 @@ __device__ __forceinline__ Dist make_dist(const Geom& g, const ModParams& m, con
   return Dist{(float)(at.t - first.t), (float)(at.h - first.h), (float)(at.w - first.w),
               g.T > 1 ? scale * m.dist[0] : 0.f, g.H > 1 ? scale * m.dist[1] : 0.f, g.W > 1 ? scale * m.dist[2] : 0.f};
 }
-// y[q .. q + 3] += u + w terms, on packed pairs.
+// y[q .. q + 3] += u + w terms (SET: = instead), on packed pairs.
+template <bool SET>
 __device__ __forceinline__ void add4(float* y, float u, float w0, float w1, float w2, float w3) {
-  const float2 a = __fadd2_rn(make_float2(y[0], y[1]), __fadd2_rn(bc(u), make_float2(w0, w1)));
-  const float2 b = __fadd2_rn(make_float2(y[2], y[3]), __fadd2_rn(bc(u), make_float2(w2, w3)));
+  float2 a = __fadd2_rn(bc(u), make_float2(w0, w1)), b = __fadd2_rn(bc(u), make_float2(w2, w3));
+  if (!SET) {
+    a = __fadd2_rn(make_float2(y[0], y[1]), a);
+    b = __fadd2_rn(make_float2(y[2], y[3]), b);
+  }
   y[0] = a.x; y[1] = a.y; y[2] = b.x; y[3] = b.y;
 }
 template <int N>
@@ -331,7 +335,7 @@ __device__ __forceinline__ void axis_distance(float* y, const float* d, float at
 // operations a column. Chunks that are a line (sequences) take two. Axis
 // after axis, seven with the table reads, serves the other shapes and passes
 // over axes of weight zero.
-template <int N>
+template <int N, bool SET = false>
 __device__ __forceinline__ void add_distance(const Geom& g, float* y, const Table* tab, int first, const Dist& p) {
   if (g.cw == 4 || g.cw == 8) {
     float w[8];
@@ -343,9 +347,9 @@ __device__ __forceinline__ void add_distance(const Geom& g, float* y, const Tabl
       const float2 d = *reinterpret_cast<const float2*>(&tab->group[first / 4 + q]);
       const float u = fmaf(p.nh, fabsf(p.h - d.y), p.nt * fabsf(p.t - d.x));
       if ((q & 1) && wide)
-        add4(y + 4 * q, u, w[4], w[5], w[6], w[7]);
+        add4<SET>(y + 4 * q, u, w[4], w[5], w[6], w[7]);
       else
-        add4(y + 4 * q, u, w[0], w[1], w[2], w[3]);
+        add4<SET>(y + 4 * q, u, w[0], w[1], w[2], w[3]);
     }
     return;
   }
@@ -354,12 +358,16 @@ __device__ __forceinline__ void add_distance(const Geom& g, float* y, const Tabl
     const float u = fmaf(p.nh, fabsf(p.h), g.ct == 64 ? p.nw * fabsf(p.w) : p.nt * fabsf(p.t));
     const float a0 = at - (float)first;
 #pragma unroll
-    for (int q = 0; q < N; ++q) y[q] = fmaf(fabsf(a0 - (float)q), n, y[q]);
+    for (int q = 0; q < N; ++q) y[q] = SET ? fabsf(a0 - (float)q) * n : fmaf(fabsf(a0 - (float)q), n, y[q]);
     if (u != 0.f) {
 #pragma unroll
       for (int q = 0; q < N; ++q) y[q] += u;
     }
     return;
+  }
+  if (SET) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) y[q] = 0.f;
   }
   if (p.nt != 0.f) axis_distance<N>(y, tab->d[0] + first, p.t, p.nt);
   if (p.nh != 0.f) axis_distance<N>(y, tab->d[1] + first, p.h, p.nh);
