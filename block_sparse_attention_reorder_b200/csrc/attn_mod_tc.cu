@@ -429,12 +429,15 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       return true;
     };
+    // Whether some row of the warp is no visible token: its scores may be
+    // anything and must not pick the form of tanh.
+    const bool dead_rows = __any_sync(0xffffffffu, !row.live);
     bool fresh = true;  // some row of the warp has seen no key yet
     uint32_t e = L > 0 ? ulist[0] : 0u, ext = L > 0 ? uext[0] : 0u;
     for (int n = 0; n < L; ++n) {
       const bool keep = ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
       unsigned long long vis = ~0ull;
-      bool partial = false;
+      bool partial = false, clear = false;
       mod::Dist dist{};
       if (BIAS || (ext & mod::kSpecial)) {
         const mod::Coord f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
@@ -454,6 +457,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             vis = mod::visible_box(g, &tab->col, 0, vt, g.H - f.h, g.W - f.w);
             if (ext & mod::kDoc) vis &= mod::visible_doc(M, step_chunk(e), row.id);
             partial = __any_sync(0xffffffffu, vis != ~0ull);
+            clear = partial && ((ext & mod::kHidden) || dead_rows);
           }
         }
       }
@@ -474,7 +478,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             uint32_t sr[32];
             const uint32_t see = (uint32_t)(vis >> (32 * h));
             tc::tmem_ld32_wait(sbuf + 32 * h, sr);
-            if (partial) mod::set_unseen<32>(sr, see, 0.f);
+            if (clear) mod::set_unseen<32>(sr, see, 0.f);
             mod::tanh_scores<32>(sr, k);
             mod::add_distance<32>(g, reinterpret_cast<float*>(sr), &tab->col, 32 * h, dist);
             if (partial) mod::set_unseen<32>(sr, see, -INFINITY);
@@ -548,7 +552,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           for (bool measure = fresh; !done; measure = true) {
             tc::tmem_ld64_wait(sbuf, sr);
             if (CAP) {
-              if (partial) mod::set_unseen<64>(sr, vis, 0.f);
+              if (clear) mod::set_unseen<64>(sr, vis, 0.f);
               mod::tanh_scores<64>(sr, k);
             }
             if (BIAS) mod::add_distance<64>(g, reinterpret_cast<float*>(sr), &tab->col, 0, dist);

@@ -155,9 +155,13 @@ rope_kernel(const __grid_constant__ RopeParams P) {
           at = P.pos[((size_t)b * g.L + n) * 3 + a];
         }
         const int hi = (int)(((unsigned long long)at * f) >> 32);  // the turn in [-1/2, 1/2), in 2^-32
+        // fp32 holds 24 of the 32 bits; the rest turns (cos, sin) to first order.
+        const float top = (float)hi;
+        const float rest = (float)(int)((long long)hi - (long long)top) * (float)(M_PI * 0x1p-31);
         float s, c;
-        sincospif((float)hi * 0x1p-31f, &s, &c);
-        table[v * R + p] = make_float2(c * P.amp, s * P.amp * P.sign);
+        sincospif(top * 0x1p-31f, &s, &c);
+        const float s1 = fmaf(c, rest, s), c1 = fmaf(-s, rest, c);
+        table[v * R + p] = make_float2(c1 * P.amp, s1 * P.amp * P.sign);
       }
     }
     __syncthreads();
@@ -303,7 +307,7 @@ bsattn_status run(RopeParams& prm, int ntensor, bool pool, cudaStream_t st) {
   if (g.B > 65535 || gx > 0x7fffffffLL) return BSATTN_ERR_UNSUPPORTED;
   const int box = g.ct > g.ch ? (g.ct > g.cw ? g.ct : g.cw) : (g.ch > g.cw ? g.ch : g.cw);
   const size_t smem = (size_t)(prm.pos ? g.cr : box) * prm.npairs * sizeof(float2);  // <= 32 KB
-  if (pool) {  // with the exchange buffer above the default 48 KB at the largest
+  if (pool && smem > 14 * 1024) {  // with the exchange buffer (33 KB at most) above the default 48 KB
     if (cudaFuncSetAttribute(rope_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024) != cudaSuccess)
       return BSATTN_ERR_CUDA;
   }
@@ -342,8 +346,8 @@ bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r) {
 // x modulo 1 (x >= 0), in units of 2^-64.
 static unsigned long long fraction64(double x) {
   x -= floor(x);
-  const double hi = floor(ldexp(x, 32));
-  const double lo = floor(ldexp(ldexp(x, 32) - hi, 32));
+  const double hi = floor(x * 0x1p32);
+  const double lo = floor((x * 0x1p32 - hi) * 0x1p32);
   return ((unsigned long long)hi << 32) | (unsigned long long)lo;
 }
 
@@ -366,8 +370,10 @@ bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv
       const double s = r->factor[a];
       double base = r->base;
       if (r->scaling == BSATTN_ROPE_SCALE_NTK && d > 2) base *= pow(s, (double)d / (d - 2));
+      // exp2 of the rounded exponent: within 1e-7 of a radian at position 2^31.
+      const double per_pair = d > 0 ? -2.0 * log2(base) / d : 0.0;
       for (int i = 0; i < d / 2; ++i) {
-        double f = pow(base, -2.0 * i / d);
+        double f = exp2(per_pair * i);
         if (r->scaling == BSATTN_ROPE_SCALE_LINEAR) f /= s;
         if (r->scaling == BSATTN_ROPE_SCALE_BY_PARTS) {
           double keep = (r->original[a] * f / kTwoPi - r->slow) / (r->fast - r->slow);
