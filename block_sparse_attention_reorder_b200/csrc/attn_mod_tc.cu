@@ -12,7 +12,7 @@
 //  * The rules cost 3 to 10 FMA-pipe operations a score on top of the
 //    softmax's four; masks and their tables are fetched while S is computed.
 //  * The reference m of 2^(x - m) is set by the first step that shows the row
-//    a key and moves only when a score grows by more than 2^100, for which
+//    a key and moves only when a score grows by more than 2^70, for which
 //    fp32's exponent range has room in the sums and in bf16 P. So no step
 //    waits for its row maximum: the step's sum shows whether a term was too
 //    large, and then, hardly ever, the step is taken again with the maximum,
@@ -39,11 +39,13 @@ constexpr uint32_t kColS0 = 0, kColS1 = 64, kColO = 128;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
 constexpr long long kTestWaitLimit = 2000000LL;  // ~1 ms, with the testing hook on
 // A row's reference m is put kAbove over a maximum and stays until a score
-// exceeds m by kRaise (log2 units): probabilities between 2^-40 and 2^60
-// times their rounding are exact in fp32 sums and bf16 alike, and terms that
-// fall below fp32's range are under 2^-86 of the largest.
-constexpr float kAbove = 40.f, kRaise = 60.f;
-constexpr float kSumLimit = 0x1p60f;  // no term of a smaller sum exceeds m + kRaise
+// exceeds m by kRaise (log2 units), i.e. until the maximum grows by 70: fp32
+// sums and bf16 P, both with fp32's exponent range, hold all of 2^-40 .. 2^30
+// with values of V from 2^-80 to 2^80, and terms that fall below the range are
+// under 2^-86 of the largest.
+constexpr float kAbove = 40.f, kRaise = 30.f;
+constexpr float kSumLimit = 0x1p30f;  // no term of a smaller sum exceeds m + kRaise
+constexpr float kAboveUnit = 0x1p40f;
 
 struct Params {
   Geom g;
@@ -536,7 +538,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // A row that has seen no key yet has m = -inf and only -inf scores.
             const float2 c2 = mod::bc(c), nm2 = mod::bc(m == -INFINITY ? 0.f : -m);
             float2 ls2[4] = {mod::bc(0.f), mod::bc(0.f), mod::bc(0.f), mod::bc(0.f)};
-  #pragma unroll
+#pragma unroll
             for (int q = 0; q < 32; ++q) {
               const float2 x = __ffma2_rn(mod::pair(sr + 2 * q), c2, nm2);
               const float2 p = make_float2(tc::ex2(x.x), tc::ex2(x.y));
@@ -559,7 +561,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (partial) mod::set_unseen<64>(sr, vis, -INFINITY);
             if (measure) {
               float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  #pragma unroll
+#pragma unroll
               for (int q = 0; q < 32; ++q)
                 mx4[q & 3] = tc::fmax3(mx4[q & 3], __uint_as_float(sr[2 * q]), __uint_as_float(sr[2 * q + 1]));
               const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
@@ -574,7 +576,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
           l = l * alpha + sum;
         } else {
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < 32; ++q) pk[q] = 0u;
         }
         tc::tmem_st32(sbuf, pk);  // P_n over the first 32 columns of S_n
@@ -623,7 +625,8 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     }
     if (P.lse && row_exists) {
-      const float lse_r = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      // In terms of the maximum, so that no rounding of m's size enters.
+      const float lse_r = l > 0.f ? ((m - kAbove) + log2f(l * kAboveUnit)) * 0.69314718055994531f : -INFINITY;
       if (NAT) {
         if (tokrow[r] >= 0) P.lse[bh * (size_t)g.L + (size_t)tokrow[r]] = lse_r;
       } else {

@@ -269,7 +269,7 @@ bool ok_ptr(const void* x) { return x != nullptr && aligned16(x); }
 
 bsattn_status check_mod(const bsattn_score_mod* m) {
   if (!m) return BSATTN_ERR_INVALID_ARG;
-  if (!(m->softcap >= 0.f) || !isfinite(m->softcap)) return BSATTN_ERR_INVALID_ARG;
+  if (m->softcap != 0.f && !(m->softcap >= 1e-6f && m->softcap <= 1e30f)) return BSATTN_ERR_INVALID_ARG;
   const float d[3] = {m->dist_t, m->dist_h, m->dist_w};
   for (float x : d)
     if (!(x >= 0.f) || !isfinite(x)) return BSATTN_ERR_INVALID_ARG;

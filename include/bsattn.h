@@ -405,7 +405,7 @@ bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const 
  * finite. A sequence is a grid of one column (T = length, H = W = 1, tiles
  * of (64, 1, 1)). */
 typedef struct {
-  float softcap;                 /* 0: off; else > 0, finite                  */
+  float softcap;                 /* 0: off; else in [1e-6, 1e30]              */
   float dist_t, dist_h, dist_w;  /* >= 0, finite                              */
   const float* slopes;           /* NULL: off; device fp32 [heads], finite    */
   int causal;                    /* 0 or 1                                    */
@@ -476,7 +476,8 @@ bsattn_status attn_layer_mod(const bsattn_plan* plan, const bsattn_rope* rope, c
  * counterpart); they let tests reach the failure paths without faulting a GPU.
  *
  * attn_testing_force_timeout(1): attention forward launches made afterwards
- * in this process (attn_forward, attn_forward_natural, attn_layer) cap the
+ * in this process (attn_forward, attn_forward_natural, attn_layer and their
+ * _mod forms) cap the
  * kernel's abortable waits at about 1 ms and make each CTA's MMA-issuing
  * thread first wait on a barrier nothing arrives at, so every CTA takes its
  * bounded-wait timeout path: it records BSATTN_ERR_TIMEOUT in the plan's

@@ -462,7 +462,28 @@ def _mod_calls(bs, c, mod, ws="mod_forward"):
                                 plan.workspace(ws) if ws else None)
 
 
-@pytest.mark.parametrize("kw", [dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
+def test_timeouts_and_bad_lists_are_reported(bs):
+    c = Case(bs, "ragged", "all")
+    plan, ws = c.plan, c.plan.workspace("mod_forward")
+    run = lambda idx, o: bs.attn_forward_natural_mod(plan, c.mod, c.q.cuda(), c.k.cuda(), c.v.cuda(), idx, c.cnt, o, ws)  # noqa: E731
+    o = torch.empty(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")
+    bs.attn_testing_force_timeout(True)
+    try:
+        run(c.idx, o)
+        assert bs.attn_check_device_status(plan) == 4
+    finally:
+        bs.attn_testing_force_timeout(False)
+    run(c.idx, o)  # and works again
+    assert bs.attn_check_device_status(plan) == 0
+    bad = c.idx.clone()
+    bad[0, 1, 0, 0] = plan.N  # out of range: skipped and reported
+    again = torch.empty_like(o)
+    run(bad, again)
+    assert bs.attn_check_device_status(plan) == 5
+    assert torch.equal(again[1:], o[1:])
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=1e-7), dict(softcap=1e31), dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
                                 dict(dist=(1.0, -1.0, 0.0)), dict(dist=(float("nan"), 0.0, 0.0)), dict(prefix=True)])
 def test_bad_rules_are_refused(bs, kw):
     c = Case(bs, "ragged", "off")
