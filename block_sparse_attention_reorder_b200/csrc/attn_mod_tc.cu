@@ -65,7 +65,27 @@ struct Params {
   int pdim[3];
   long long wait_limit;
   int stall;  // testing: the MMA thread first waits on a barrier nothing arrives at
+  int parts;  // CTAs that share a query block's steps
+  float* part_o;   // parts > 1: [blocks, parts, 128, D] unnormalised O
+  float2* part_ml; // [blocks, parts, 128] (m, l) of each row; l = 0: saw no key
 };
+
+// A work item's halves; with natural outputs chunks of padded rows only are
+// left out. False: nothing to do.
+template <bool NAT>
+__device__ __forceinline__ bool work_halves(const Params& P, int item, int* i0, int* i1, int* c0, int* c1) {
+  const Geom& g = P.g;
+  block_halves(g, P.pair_axis, P.pdim, item, i0, i1, c0, c1);
+  if (NAT && g.nchunk > 1) {
+    if (*i1 >= 0 && !chunk_is_real(g, *i1, *c1)) *i1 = -1;
+    if (!chunk_is_real(g, *i0, *c0)) {
+      if (*i1 < 0) return false;
+      *c0 = *c1;
+      *i1 = -1;
+    }
+  }
+  return true;
+}
 
 template <int D, bool FP8>
 struct Cfg {
@@ -116,7 +136,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // Cap and bias together: 32 columns at a time in a loop, with P in two
   // halves (16 columns each, 32 apart). Straight-line code for all 64 stalls
   // on instruction fetch (PLACEHOLDER).
-  constexpr bool kSplit = CAP && BIAS;
+  constexpr bool kHalves = CAP && BIAS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -142,16 +162,9 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   const Geom& g = P.g;
   const ModParams& M = P.mod;
+  const int item = blockIdx.x / P.parts, part = blockIdx.x % P.parts;
   int i0, i1, c0, c1;
-  block_halves(g, P.pair_axis, P.pdim, blockIdx.x, &i0, &i1, &c0, &c1);
-  if (NAT && g.nchunk > 1) {  // chunks of padded rows only are never written to the natural layout
-    if (i1 >= 0 && !chunk_is_real(g, i1, c1)) i1 = -1;
-    if (!chunk_is_real(g, i0, c0)) {
-      if (i1 < 0) return;  // uniform over the CTA, before any setup
-      c0 = c1;
-      i1 = -1;
-    }
-  }
+  if (!work_halves<NAT>(P, item, &i0, &i1, &c0, &c1)) return;  // uniform over the CTA, before any set-up
   const int head = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * g.Hh + head;
   const bool has1 = i1 >= 0;
@@ -246,7 +259,13 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  if (P.parts > 1) {  // this CTA's share of the steps
+    const int lo = L * part / P.parts;
+    L = L * (part + 1) / P.parts - lo;
+    ulist += lo;
+    uext += lo;
+  }
 
   // ------------------------------------------------------------ roles
   if (warp == 4) {
@@ -374,7 +393,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t dv = tc::smem_desc(sb + C::OFF_V + s * C::V_BYTES + kk * 2048, 8192, 1024, tc::kLayoutSW128);
-          tc::mma_ts_f16_warp(lead, tmem + kColO, pA + (kSplit && kk >= 2 ? 16 : 0) + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_ts_f16_warp(lead, tmem + kColO, pA + (kHalves && kk >= 2 ? 16 : 0) + kk * 8, dv, idPV, (n > 0 || kk > 0) ? 1u : 0u);
         }
         tc::mma_commit_warp(lead, bar_pvdone(n & 1));
         if (n + 2 < L && !issue_S(n + 2)) {
@@ -431,9 +450,11 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       return true;
     };
-    // Whether some row of the warp is no visible token: its scores may be
-    // anything and must not pick the form of tanh.
-    const bool dead_rows = __any_sync(0xffffffffu, !row.live);
+    // Whether scores of the warp may hold anything in masked places without
+    // hidden keys: rows that are no visible token, and, in chunks of fewer than
+    // 64 tokens, key rows that no load fills. They must not pick the form of
+    // tanh.
+    const bool odd_rows = __any_sync(0xffffffffu, !row.live) || g.cr < 64;
     bool fresh = true;  // some row of the warp has seen no key yet
     uint32_t e = L > 0 ? ulist[0] : 0u, ext = L > 0 ? uext[0] : 0u;
     for (int n = 0; n < L; ++n) {
@@ -458,8 +479,9 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
             vis = mod::visible_box(g, &tab->col, 0, vt, g.H - f.h, g.W - f.w);
             if (ext & mod::kDoc) vis &= mod::visible_doc(M, step_chunk(e), row.id);
+            if (!row.live) vis = 0;
             partial = __any_sync(0xffffffffu, vis != ~0ull);
-            clear = partial && ((ext & mod::kHidden) || dead_rows);
+            clear = partial && ((ext & mod::kHidden) || odd_rows);
           }
         }
       }
@@ -471,7 +493,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t sbuf = tmem + lane_base + ((n & 1) ? kColS1 : kColS0);
-      if constexpr (kSplit) {
+      if constexpr (kHalves) {
         const float k = FP8 ? kq * ksc : kq;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -604,47 +626,63 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool real = row_exists && (r & 63) < g.cr && row.at.t < g.T && row.at.h < g.H && row.at.w < g.W;
       tokrow[r] = real ? (row.at.t * g.H + row.at.h) * g.W + row.at.w : -1;
     }
-    if (!row.live) l = 0.f;  // padded or hidden: a zero row
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
-#pragma unroll
-    for (int col = 0; col < D; col += 32) {
-      uint32_t o[32];
+    if (!row.live || !ok) l = 0.f;  // padded or hidden: a zero row
+    if (P.parts > 1) {
+      const size_t at = (((bh * (gridDim.x / P.parts) + item) * P.parts + part) * 128 + r);
+      P.part_ml[at] = make_float2(m, l);
       if (ok && L > 0) {
-        tc::tmem_ld32_wait(tmem + lane_base + kColO + col, o);
-      }
-      if (!(ok && L > 0 && row.live)) {  // whatever the row holds, NaN included
 #pragma unroll
-        for (int q = 0; q < 32; ++q) o[q] = 0u;
-      }
-      uint32_t w[16];
+        for (int col = 0; col < D; col += 16) {
+          uint32_t o[16];
+          tc::tmem_ld16_wait(tmem + lane_base + kColO + col, o);
+          if (l == 0.f) continue;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) w[q] = mod::pack(__fmul2_rn(mod::pair(o + 2 * q), mod::bc(inv)));
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    }
-    if (P.lse && row_exists) {
-      // In terms of the maximum, so that no rounding of m's size enters.
-      const float lse_r = l > 0.f ? ((m - kAbove) + log2f(l * kAboveUnit)) * 0.69314718055994531f : -INFINITY;
-      if (NAT) {
-        if (tokrow[r] >= 0) P.lse[bh * (size_t)g.L + (size_t)tokrow[r]] = lse_r;
-      } else {
-        P.lse[(size_t)tiled_row(half ? i1 : i0, half ? c1 : c0) + (r & 63)] = lse_r;
+          for (int q = 0; q < 4; ++q)
+            reinterpret_cast<uint4*>(P.part_o + at * D + col)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
       }
-    }
-    sync_softmax();
-    constexpr int CPR = D / 8;  // 16-byte pieces per row
-    const int rows = has1 ? 128 : 64;
-    for (int e2 = tid; e2 < rows * CPR; e2 += kSoftmaxThreads) {
-      const int rr = e2 / CPR, cc = e2 % CPR;
-      const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_K + rr * C::O_PITCH + cc * 16);
-      if (NAT) {
-        const int n = tokrow[rr];
-        if (n >= 0) reinterpret_cast<uint4*>(P.o + (((size_t)b * g.L + n) * g.Hh + head) * D)[cc] = val;
-      } else {
-        uint4* og = reinterpret_cast<uint4*>(P.o + (size_t)tiled_row(rr >> 6 ? i1 : i0, rr >> 6 ? c1 : c0) * D);
-        og[(rr & 63) * CPR + cc] = val;
+    } else {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
+#pragma unroll
+      for (int col = 0; col < D; col += 32) {
+        uint32_t o[32];
+        if (ok && L > 0) {
+          tc::tmem_ld32_wait(tmem + lane_base + kColO + col, o);
+        }
+        if (!(ok && L > 0 && row.live)) {  // whatever the row holds, NaN included
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0u;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) w[q] = mod::pack(__fmul2_rn(mod::pair(o + 2 * q), mod::bc(inv)));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      }
+      if (P.lse && row_exists) {
+        // In terms of the maximum, so that no rounding of m's size enters.
+        const float lse_r = l > 0.f ? ((m - kAbove) + log2f(l * kAboveUnit)) * 0.69314718055994531f : -INFINITY;
+        if (NAT) {
+          if (tokrow[r] >= 0) P.lse[bh * (size_t)g.L + (size_t)tokrow[r]] = lse_r;
+        } else {
+          P.lse[(size_t)tiled_row(half ? i1 : i0, half ? c1 : c0) + (r & 63)] = lse_r;
+        }
+      }
+      sync_softmax();
+      constexpr int CPR = D / 8;  // 16-byte pieces per row
+      const int rows = has1 ? 128 : 64;
+      for (int e2 = tid; e2 < rows * CPR; e2 += kSoftmaxThreads) {
+        const int rr = e2 / CPR, cc = e2 % CPR;
+        const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_K + rr * C::O_PITCH + cc * 16);
+        if (NAT) {
+          const int n = tokrow[rr];
+          if (n >= 0) reinterpret_cast<uint4*>(P.o + (((size_t)b * g.L + n) * g.Hh + head) * D)[cc] = val;
+        } else {
+          uint4* og = reinterpret_cast<uint4*>(P.o + (size_t)tiled_row(rr >> 6 ? i1 : i0, rr >> 6 ? c1 : c0) * D);
+          og[(rr & 63) * CPR + cc] = val;
+        }
       }
     }
   }
@@ -655,6 +693,59 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (warp == 5) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of each query block: with M the greatest m + log2(l), w =
+// 2^(m - M), l = sum w l, O = sum w O / l. 16 threads a row (D = 64: 8), eight
+// features each.
+constexpr int kJoinThreads = 256;
+template <int D, bool NAT>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ Params P) {
+  constexpr int CPR = D / 8;
+  const Geom& g = P.g;
+  const int head = blockIdx.y, b = blockIdx.z;
+  const size_t bh = (size_t)b * g.Hh + head;
+  int i0, i1, c0, c1;
+  if (!work_halves<NAT>(P, blockIdx.x, &i0, &i1, &c0, &c1)) return;
+  for (int e = threadIdx.x; e < 128 * CPR; e += kJoinThreads) {
+    const int r = e / CPR, piece = e % CPR, half = r >> 6;
+    if (half && i1 < 0) continue;
+    const int tile = half ? i1 : i0, chunk = half ? c1 : c0;
+    size_t out;  // row of O and lse
+    if (NAT) {
+      const uint32_t code = chunk_row_code(g, r & 63);
+      const mod::Coord f = mod::chunk_first(g, P.mod, mod::pack_tile(g, P.mod, tile), chunk_origin(g, chunk));
+      const int t = f.t + (int)(code & 0xffu), h = f.h + (int)((code >> 8) & 0xffu), w = f.w + (int)((code >> 16) & 0xffu);
+      if ((r & 63) >= g.cr || t >= g.T || h >= g.H || w >= g.W) continue;
+      out = (size_t)(t * g.H + h) * g.W + w;
+    } else {
+      out = (bh * g.N + tile) * g.V + 64 * chunk + (r & 63);
+    }
+    const size_t at = ((bh * gridDim.x + blockIdx.x) * P.parts) * 128 + r;
+    float M = -INFINITY;
+    for (int p = 0; p < P.parts; ++p) {
+      const float2 ml = P.part_ml[at + p * 128];
+      if (ml.y != 0.f) M = fmaxf(M, ml.x + log2f(ml.y));
+    }
+    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < P.parts; ++p) {
+      const float2 ml = P.part_ml[at + p * 128];
+      if (ml.y == 0.f) continue;
+      const float w = exp2f(ml.x - M);
+      l = fmaf(w, ml.y, l);
+      const float4* src = reinterpret_cast<const float4*>(P.part_o + (at + p * 128) * D) + 2 * piece;
+      const float4 x = src[0], y = src[1];
+      o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]); o[2] = fmaf(w, x.z, o[2]); o[3] = fmaf(w, x.w, o[3]);
+      o[4] = fmaf(w, y.x, o[4]); o[5] = fmaf(w, y.y, o[5]); o[6] = fmaf(w, y.z, o[6]); o[7] = fmaf(w, y.w, o[7]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const uint4 val = make_uint4(mod::pack(make_float2(o[0] * inv, o[1] * inv)), mod::pack(make_float2(o[2] * inv, o[3] * inv)),
+                                 mod::pack(make_float2(o[4] * inv, o[5] * inv)), mod::pack(make_float2(o[6] * inv, o[7] * inv)));
+    __nv_bfloat16* dst = P.o + (NAT ? (((size_t)b * g.L + out) * g.Hh + head) * D : out * D);
+    reinterpret_cast<uint4*>(dst)[piece] = val;
+    if (P.lse && piece == 0)
+      P.lse[NAT ? bh * (size_t)g.L + out : out] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -680,8 +771,9 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
   auto kern = attn_mod_tc_kernel<D, FP8, NAT, CAP, BIAS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  dim3 grid(attention_items(p), p->desc.heads, p->desc.B);
-  kern<<<grid, kThreads, smem, st>>>(mq, mk, mv, prm);
+  const int items = attention_items(p);
+  kern<<<dim3(items * prm.parts, p->desc.heads, p->desc.B), kThreads, smem, st>>>(mq, mk, mv, prm);
+  if (prm.parts > 1) attn_join_kernel<D, NAT><<<dim3(items, p->desc.heads, p->desc.B), kJoinThreads, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
@@ -697,9 +789,30 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
 
 }  // namespace
 
+// Few query blocks leave most of the GPU idle while each walks its list: up to
+// eight CTAs then share a block's steps, two per SM at most over the grid and
+// four steps each at least, and a second kernel joins their parts. PLACEHOLDER
+static int steps_bound(const bsattn_plan* p) {
+  // The union of two lists of one-chunk tiles, or one list of tiles times their chunks.
+  return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+}
+static int attention_parts(const bsattn_plan* p) {
+  const long long blocks = (long long)attention_items(p) * p->desc.heads * p->desc.B;
+  long long parts = 2 * 148 / blocks;
+  if (parts > steps_bound(p) / 4) parts = steps_bound(p) / 4;
+  return parts < 2 ? 1 : parts > 8 ? 8 : (int)parts;
+}
+size_t attention_mod_workspace_bytes(const bsattn_plan* p) {
+  const int parts = attention_parts(p);
+  if (parts == 1) return 0;
+  const size_t rows = (size_t)attention_items(p) * p->desc.heads * p->desc.B * parts * 128;
+  return rows * ((size_t)p->desc.head_dim * sizeof(float) + sizeof(float2));
+}
+
 bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
                                    const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
-                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, cudaStream_t st, AttnLayout lay) {
+                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, void* ws, cudaStream_t st,
+                                   AttnLayout lay) {
   if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
   Params prm;
   prm.g = make_geom(p);
@@ -713,9 +826,13 @@ bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, c
   prm.lse = lse;
   prm.scale = p->scale;
   prm.err = p->d_err;
-  // The union of two lists of one-chunk tiles, or one list of tiles times their chunks.
-  prm.umax = p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax)
-                            : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+  prm.umax = steps_bound(p);
+  prm.parts = ws ? attention_parts(p) : 1;
+  prm.part_o = (float*)ws;
+  prm.part_ml = nullptr;
+  if (prm.parts > 1)
+    prm.part_ml = (float2*)(prm.part_o + (size_t)attention_items(p) * p->desc.heads * p->desc.B * prm.parts * 128 *
+                                             p->desc.head_dim);
   prm.bm_words = (p->N + 31) / 32;
   prm.pair_axis = pair_axis_of(p);
   prm.stall = bsattn_testing_timeout_forced() ? 1 : 0;

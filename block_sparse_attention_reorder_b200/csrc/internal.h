@@ -184,10 +184,13 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
                                const int32_t* idx, const int32_t* cnt, __nv_bfloat16* o,
                                float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
                                AttnLayout lay);
-// The same under score rules (csrc/attn_mod_tc.cu).
+// The same under score rules (csrc/attn_mod_tc.cu). ws: scratch of
+// attention_mod_workspace_bytes, or null (then no CTAs share a query block).
+size_t attention_mod_workspace_bytes(const bsattn_plan* p);
 bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
                                    const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
-                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, cudaStream_t st, AttnLayout lay);
+                                   const int32_t* cnt, __nv_bfloat16* o, float* lse, void* ws, cudaStream_t st,
+                                   AttnLayout lay);
 // Tile axis (0 = t, 1 = h, 2 = w) along which two 64-token tiles are stacked
 // into one 128-row block (attention: query tiles; dK/dV: key tiles). Top-k and
 // top-p: t, whose neighbouring tiles keep the most key tiles in common on the

@@ -54,8 +54,20 @@ BwdModWs carve_backward_mod(const bsattn_plan* p, Carve& c) {
   return w;
 }
 
+struct FwdModWs {
+  DocWs doc;
+  void* parts;
+};
+FwdModWs carve_forward_mod(const bsattn_plan* p, Carve& c) {
+  FwdModWs w;
+  w.doc = carve_doc(p, c);
+  w.parts = c.take(attention_mod_workspace_bytes(p));
+  return w;
+}
+
 struct LayerModWs {
   DocWs doc;
+  void* parts;
   __nv_bfloat16 *q, *k;  // rotated
   uint8_t *qc, *kc;      // e4m3 tile codes
   float *qs, *ks;
@@ -68,6 +80,7 @@ LayerModWs carve_layer_mod(const bsattn_plan* p, Carve& c) {
   const size_t codes = p->desc.qk_fp8 ? bh * p->N * p->V * D : 0;
   LayerModWs w;
   w.doc = carve_doc(p, c);
+  w.parts = c.take(attention_mod_workspace_bytes(p));
   w.q = (__nv_bfloat16*)c.take(bh * p->L * D * 2);
   w.k = (__nv_bfloat16*)c.take(bh * p->L * D * 2);
   w.qc = (uint8_t*)c.take(codes);
@@ -342,14 +355,20 @@ bsattn_status forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const
   if (p->desc.qk_fp8 && (!ok_ptr(qs) || !ok_ptr(ks))) return BSATTN_ERR_INVALID_ARG;
   bsattn_status s = check_mod(m);
   if (s) return s;
-  DocWs w;
-  if ((s = carve_call_doc(p, m, ws, ws_bytes, &w))) return s;
+  Carve size(nullptr);
+  carve_forward_mod(p, size);
+  FwdModWs w{};
+  if (ws || m->doc) {
+    if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+    Carve c(ws);
+    w = carve_forward_mod(p, c);
+  }
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
-  if ((s = launch_doc_prep(p, m, w, (cudaStream_t)stream))) return s;
-  const ModParams d = device_mod(p, m, w);
+  if ((s = launch_doc_prep(p, m, w.doc, (cudaStream_t)stream))) return s;
+  const ModParams d = device_mod(p, m, w.doc);
   return launch_attention_mod(p, d, q, k, qs, ks, (const __nv_bfloat16*)v, idx, cnt, (__nv_bfloat16*)o, lse,
-                              (cudaStream_t)stream, lay);
+                              w.parts, (cudaStream_t)stream, lay);
 }
 
 }  // namespace
@@ -358,11 +377,13 @@ extern "C" {
 
 bsattn_status attn_mod_info(const bsattn_plan* p, bsattn_mod_info* o) {
   if (!p || !o) return BSATTN_ERR_INVALID_ARG;
-  Carve a(nullptr), b(nullptr), c(nullptr);
+  Carve a(nullptr), f(nullptr), b(nullptr), c(nullptr);
   carve_doc(p, a);
+  carve_forward_mod(p, f);
   carve_backward_mod(p, b);
   carve_layer_mod(p, c);
-  o->scores_workspace_bytes = o->forward_workspace_bytes = a.off;
+  o->scores_workspace_bytes = a.off;
+  o->forward_workspace_bytes = f.off;
   o->backward_workspace_bytes = b.off;
   o->layer_workspace_bytes = c.off;
   return BSATTN_OK;
@@ -474,7 +495,7 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
   }
   if (m)
     return launch_attention_mod(p, d, qa, ka, w.qs, w.ks, (const __nv_bfloat16*)v_nat, idx, cnt, (__nv_bfloat16*)o_nat,
-                                lse_nat, st, AttnLayout::Natural);
+                                lse_nat, w.parts, st, AttnLayout::Natural);
   return launch_attention(p, qa, ka, w.qs, w.ks, (const __nv_bfloat16*)v_nat, idx, cnt, (__nv_bfloat16*)o_nat, lse_nat,
                           nullptr, 0, st, AttnLayout::Natural);
 }

@@ -438,7 +438,8 @@ bsattn_status attn_mod_scores(const bsattn_plan* plan, const bsattn_score_mod* m
  * bias and masks are applied in fp32 inside the kernel, and key chunks that
  * the rules hide from a whole query block are not visited). Padded rows of
  * the tiled layout get O = 0, lse = -inf. `ws`: forward_workspace_bytes; may
- * be NULL without doc. */
+ * be NULL without doc, and then small problems, whose query blocks several
+ * CTAs share through it, take longer and round differently. */
 bsattn_status attn_forward_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
                                const void* k, const float* q_scale, const float* k_scale, const void* v,
                                const int32_t* idx, const int32_t* cnt, void* o_tiled, float* lse, void* ws,

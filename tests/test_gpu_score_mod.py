@@ -232,6 +232,29 @@ def test_hidden_rows_may_hold_anything(bs, grid, rule):
     assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
+@pytest.mark.parametrize("grid", ["ragged", "ragged_d64", "tile688", "seq400"])
+def test_without_a_workspace(bs, grid):
+    """No CTAs share a query block then: the same tolerances."""
+    c = Case(bs, grid, "cap", seed=7)
+    o, lse = _nan(c.plan.natural_shape()), _nan((c.B, c.heads, c.L), torch.float32)
+    bs.attn_forward_natural_mod(c.plan, c.mod, c.q.cuda(), c.k.cuda(), c.v.cuda(), c.idx, c.cnt, o, lse_nat=lse)
+    assert bs.attn_check_device_status(c.plan) == 0
+    c.check_forward(to64(o), to64(lse), *(to64(x) for x in (c.q, c.k, c.v)))
+
+
+def test_large_and_falling_scores(bs):
+    """Scores far apart within a row, so that references move and parts of a row's keys vanish."""
+    for amp, grid in ((300.0, "seq400"), (300.0, "ragged"), (2000.0, "seq400")):
+        c = Case(bs, grid, "off", seed=8, amp=amp)
+        for order in (1, -1):  # the largest scores last, first
+            k = c.k.double().numpy()
+            k = torch.from_numpy(k * np.linspace(0, 1, c.L)[::order][None, :, None, None]).to(torch.bfloat16)
+            for ws in (None, c.plan.workspace("mod_forward")):
+                o, lse = _nan(c.plan.natural_shape()), _nan((c.B, c.heads, c.L), torch.float32)
+                bs.attn_forward_natural_mod(c.plan, c.mod, c.q.cuda(), k.cuda(), c.v.cuda(), c.idx, c.cnt, o, ws, lse_nat=lse)
+                c.check_forward(to64(o), to64(lse), *(to64(x) for x in (c.q, k, c.v)))
+
+
 @pytest.mark.parametrize("grid", ["ragged", "seq400", "tile688"])
 def test_ids_in_any_order(bs, grid):
     c = Case(bs, grid, "all", seed=3, random_docs=True)
