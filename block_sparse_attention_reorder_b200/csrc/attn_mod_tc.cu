@@ -697,56 +697,64 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 }
 
 // Joins the parts of each query block: with M the greatest m + log2(l), w =
-// 2^(m - M), l = sum w l, O = sum w O / l. 16 threads a row (D = 64: 8), eight
-// features each.
-constexpr int kJoinThreads = 256;
+// 2^(m - M), l = sum w l, O = sum w O / l. D / 8 threads a row, eight features
+// each; a CTA takes kJoinRows rows, every load of a thread in flight at once.
+constexpr int kMaxParts = 8, kJoinRows = 16;
 template <int D, bool NAT>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ Params P) {
-  constexpr int CPR = D / 8;
+__global__ void __launch_bounds__(kJoinRows * D / 8) attn_join_kernel(const __grid_constant__ Params P) {
   const Geom& g = P.g;
-  const int head = blockIdx.y, b = blockIdx.z;
+  const int head = blockIdx.y, b = blockIdx.z, item = blockIdx.x / (128 / kJoinRows);
   const size_t bh = (size_t)b * g.Hh + head;
+  const int r = blockIdx.x % (128 / kJoinRows) * kJoinRows + threadIdx.x / (D / 8), piece = threadIdx.x % (D / 8);
+  const int half = r >> 6;
   int i0, i1, c0, c1;
-  if (!work_halves<NAT>(P, blockIdx.x, &i0, &i1, &c0, &c1)) return;
-  for (int e = threadIdx.x; e < 128 * CPR; e += kJoinThreads) {
-    const int r = e / CPR, piece = e % CPR, half = r >> 6;
-    if (half && i1 < 0) continue;
-    const int tile = half ? i1 : i0, chunk = half ? c1 : c0;
-    size_t out;  // row of O and lse
-    if (NAT) {
-      const uint32_t code = chunk_row_code(g, r & 63);
-      const mod::Coord f = mod::chunk_first(g, P.mod, mod::pack_tile(g, P.mod, tile), chunk_origin(g, chunk));
-      const int t = f.t + (int)(code & 0xffu), h = f.h + (int)((code >> 8) & 0xffu), w = f.w + (int)((code >> 16) & 0xffu);
-      if ((r & 63) >= g.cr || t >= g.T || h >= g.H || w >= g.W) continue;
-      out = (size_t)(t * g.H + h) * g.W + w;
-    } else {
-      out = (bh * g.N + tile) * g.V + 64 * chunk + (r & 63);
-    }
-    const size_t at = ((bh * gridDim.x + blockIdx.x) * P.parts) * 128 + r;
-    float M = -INFINITY;
-    for (int p = 0; p < P.parts; ++p) {
-      const float2 ml = P.part_ml[at + p * 128];
-      if (ml.y != 0.f) M = fmaxf(M, ml.x + log2f(ml.y));
-    }
-    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < P.parts; ++p) {
-      const float2 ml = P.part_ml[at + p * 128];
-      if (ml.y == 0.f) continue;
-      const float w = exp2f(ml.x - M);
-      l = fmaf(w, ml.y, l);
+  if (!work_halves<NAT>(P, item, &i0, &i1, &c0, &c1) || (half && i1 < 0)) return;
+  const size_t at = ((bh * (gridDim.x / (128 / kJoinRows)) + item) * P.parts) * 128 + r;
+  float2 ml[kMaxParts];
+  float4 x[kMaxParts], y[kMaxParts];
+#pragma unroll
+  for (int p = 0; p < kMaxParts; ++p) {
+    ml[p] = p < P.parts ? P.part_ml[at + p * 128] : make_float2(0.f, 0.f);
+    if (p < P.parts) {  // unwritten where l = 0, and not used then
       const float4* src = reinterpret_cast<const float4*>(P.part_o + (at + p * 128) * D) + 2 * piece;
-      const float4 x = src[0], y = src[1];
-      o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]); o[2] = fmaf(w, x.z, o[2]); o[3] = fmaf(w, x.w, o[3]);
-      o[4] = fmaf(w, y.x, o[4]); o[5] = fmaf(w, y.y, o[5]); o[6] = fmaf(w, y.z, o[6]); o[7] = fmaf(w, y.w, o[7]);
+      x[p] = src[0];
+      y[p] = src[1];
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const uint4 val = make_uint4(mod::pack(make_float2(o[0] * inv, o[1] * inv)), mod::pack(make_float2(o[2] * inv, o[3] * inv)),
-                                 mod::pack(make_float2(o[4] * inv, o[5] * inv)), mod::pack(make_float2(o[6] * inv, o[7] * inv)));
-    __nv_bfloat16* dst = P.o + (NAT ? (((size_t)b * g.L + out) * g.Hh + head) * D : out * D);
-    reinterpret_cast<uint4*>(dst)[piece] = val;
-    if (P.lse && piece == 0)
-      P.lse[NAT ? bh * (size_t)g.L + out : out] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
+  const int tile = half ? i1 : i0, chunk = half ? c1 : c0;
+  size_t out;  // row of O and lse
+  if (NAT) {
+    const uint32_t code = chunk_row_code(g, r & 63);
+    const mod::Coord f = mod::chunk_first(g, P.mod, mod::pack_tile(g, P.mod, tile), chunk_origin(g, chunk));
+    const int t = f.t + (int)(code & 0xffu), h = f.h + (int)((code >> 8) & 0xffu), w = f.w + (int)((code >> 16) & 0xffu);
+    if ((r & 63) >= g.cr || t >= g.T || h >= g.H || w >= g.W) return;
+    out = (size_t)(t * g.H + h) * g.W + w;
+  } else {
+    out = (bh * g.N + tile) * g.V + 64 * chunk + (r & 63);
+  }
+  float M = -INFINITY;
+#pragma unroll
+  for (int p = 0; p < kMaxParts; ++p)
+    if (ml[p].y != 0.f) M = fmaxf(M, ml[p].x + log2f(ml[p].y));
+  float l = 0.f;
+  float2 o[4] = {mod::bc(0.f), mod::bc(0.f), mod::bc(0.f), mod::bc(0.f)};
+#pragma unroll
+  for (int p = 0; p < kMaxParts; ++p) {
+    if (ml[p].y == 0.f) continue;
+    const float w = exp2f(ml[p].x - M);
+    const float2 w2 = mod::bc(w);
+    l = fmaf(w, ml[p].y, l);
+    o[0] = __ffma2_rn(w2, make_float2(x[p].x, x[p].y), o[0]);
+    o[1] = __ffma2_rn(w2, make_float2(x[p].z, x[p].w), o[1]);
+    o[2] = __ffma2_rn(w2, make_float2(y[p].x, y[p].y), o[2]);
+    o[3] = __ffma2_rn(w2, make_float2(y[p].z, y[p].w), o[3]);
+  }
+  const float2 inv = mod::bc(l == 0.f ? 0.f : 1.f / l);
+  __nv_bfloat16* dst = P.o + (NAT ? (((size_t)b * g.L + out) * g.Hh + head) * D : out * D);
+  reinterpret_cast<uint4*>(dst)[piece] = make_uint4(mod::pack(__fmul2_rn(o[0], inv)), mod::pack(__fmul2_rn(o[1], inv)),
+                                                    mod::pack(__fmul2_rn(o[2], inv)), mod::pack(__fmul2_rn(o[3], inv)));
+  if (P.lse && piece == 0)
+    P.lse[NAT ? bh * (size_t)g.L + out : out] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, bool FP8, bool NAT, bool CAP, bool BIAS>
@@ -773,7 +781,8 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
     return BSATTN_ERR_CUDA;
   const int items = attention_items(p);
   kern<<<dim3(items * prm.parts, p->desc.heads, p->desc.B), kThreads, smem, st>>>(mq, mk, mv, prm);
-  if (prm.parts > 1) attn_join_kernel<D, NAT><<<dim3(items, p->desc.heads, p->desc.B), kJoinThreads, 0, st>>>(prm);
+  if (prm.parts > 1)
+    attn_join_kernel<D, NAT><<<dim3(items * (128 / kJoinRows), p->desc.heads, p->desc.B), kJoinRows * D / 8, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
@@ -800,7 +809,7 @@ static int attention_parts(const bsattn_plan* p) {
   const long long blocks = (long long)attention_items(p) * p->desc.heads * p->desc.B;
   long long parts = 2 * 148 / blocks;
   if (parts > steps_bound(p) / 4) parts = steps_bound(p) / 4;
-  return parts < 2 ? 1 : parts > 8 ? 8 : (int)parts;
+  return parts < 2 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
 }
 size_t attention_mod_workspace_bytes(const bsattn_plan* p) {
   const int parts = attention_parts(p);

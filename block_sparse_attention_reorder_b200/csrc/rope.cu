@@ -73,6 +73,7 @@ rope_kernel(const __grid_constant__ RopeParams P) {
   extern __shared__ float2 table[];   // [value][pair]
   __shared__ int rowtok[64];          // token of each row of the chunk, -1 for a padded slot
   __shared__ uint32_t rowval[64];     // its table rows along t, h, w; kHiddenRow set for a hidden token
+  __shared__ int rowpos[3][64];       // explicit positions of each row
   __shared__ int seen;                // tokens in the sums
   __shared__ float part[POOL ? kThreads * kHeads * NV : 1];
   const Geom& g = P.g;
@@ -139,7 +140,14 @@ rope_kernel(const __grid_constant__ RopeParams P) {
         if (tid % 32 == 0) atomicAdd(&seen, __popc(in));
       }
     }
-    if (P.pos) __syncthreads();
+    if (P.pos) {
+      __syncthreads();
+      for (int e = tid; e < 3 * g.cr; e += kThreads) {
+        const int a = e / g.cr, r = e % g.cr;
+        rowpos[a][r] = rowtok[r] >= 0 ? P.pos[((size_t)b * g.L + rowtok[r]) * 3 + a] : 0;
+      }
+      __syncthreads();
+    }
     // The table: thread tid takes pair tid % 64 of every second value.
     const int p = tid % 64;
     if (p < R) {
@@ -148,12 +156,7 @@ rope_kernel(const __grid_constant__ RopeParams P) {
       const unsigned long long f = P.turns[p];
       const long long at0 = (long long)P.off[a] + (a == 0 ? t0 : a == 1 ? h0 : w0);
       for (int v = tid / 64; v < vals; v += kThreads / 64) {
-        long long at = at0 + v;
-        if (P.pos) {
-          const int n = rowtok[v];
-          if (n < 0) continue;
-          at = P.pos[((size_t)b * g.L + n) * 3 + a];
-        }
+        const long long at = P.pos ? rowpos[a][v] : at0 + v;
         const int hi = (int)(((unsigned long long)at * f) >> 32);  // the turn in [-1/2, 1/2), in 2^-32
         // fp32 holds 24 of the 32 bits; the rest turns (cos, sin) to first order.
         const float top = (float)hi;
