@@ -39,6 +39,13 @@
 // product a step) and writes dQ_i = scale (dQ_i - eps_i G_i) and -(Delta_i +
 // eps_i), which the dK pass then reads.
 //
+// With the rules S takes its block operand (Q, or K) from TMEM, which leaves
+// room for one dP buffer only; it is released as soon as the softmax side has
+// read it, and dS and P go over the two halves of S. On one B200 the backward
+// of the Wan-1.3B shape takes 2.69 ms without a rule, 3.19 with the cap, 3.73
+// with cap and bias (3.58 without rules on two dP buffers, one product fewer).
+// The MMA warp issues as a whole (csrc/attn_mod_tc.cu): 3.46 -> 2.69 ms.
+//
 // Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased
 // and masked scores; the step lists are filtered as in the forward. Hidden
 // pairs take no part through selects (their scores may be NaN), and the rows
@@ -244,8 +251,10 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
   }
   __syncthreads();
-  compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
-  if constexpr (MOD) {
+  if constexpr (!MOD) {
+    compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
+  } else {
+    list_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, P.umax, scan, misc + 2);
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
@@ -837,8 +846,10 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
   }
   __syncthreads();
-  compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
-  if constexpr (MOD) {
+  if constexpr (!MOD) {
+    compact_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, uext, P.umax, scan, misc + 2);
+  } else {
+    list_steps<kThreads>(g, bmA, bmB, P.bm_words, ulist, P.umax, scan, misc + 2);
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];

@@ -17,7 +17,14 @@
 // the table serve all of its heads, a pair's two features meet in one thread
 // (in-place calls are safe), and its share of a tile's sum stays in
 // registers until one exchange at the end, in a fixed order.
-// PLACEHOLDER
+//
+// Measured on one B200 (measured copy rate 6,528 GB/s): Q and K of the
+// Wan-1.3B-shaped layer with means 59 us (291 MB, 0.75 of the copy rate; 3.7
+// waves of CTAs), the Wan-14B-shaped gradient in the half layout 576-594 us
+// (3.10 GB, 0.80-0.82), one token 3.8 us. A thread per column of all heads,
+// with angles from fp64, took 84 us, 669 us and 4-36 us; two heads a thread
+// instead of four 743 us in the half layout (twice the table reads per
+// feature, half the contiguous bytes).
 #include "internal.h"
 
 #include <math.h>

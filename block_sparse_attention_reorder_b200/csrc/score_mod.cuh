@@ -128,7 +128,7 @@ __device__ __forceinline__ void tanh_scores(uint32_t* s, float k) {
 }
 
 // A step's key chunk as the kernels keep it: tile coordinates packed with the
-// plan's bit widths (at most 18 bits: N <= 32768) and flags.
+// plan's bit widths (at most 23 bits for N <= 2^20 tiles) and flags.
 constexpr uint32_t kEdge = 1u << 31;    // padded rows
 constexpr uint32_t kCausal = 1u << 30;  // some pair of the block and the chunk is hidden by time
 constexpr uint32_t kDoc = 1u << 29;     // ids differ somewhere
@@ -177,8 +177,8 @@ __device__ __forceinline__ bool sees(const ModParams& m, int prefix, const Half&
   return true;
 }
 
-// Takes the steps that the rules hide from the block out of the compacted
-// step list (in place, order kept) and writes each step's packed coordinates
+// Takes chunks of padding and the steps that the rules hide from the block out
+// of the step list (in place, order kept) and writes each step's packed coordinates
 // and flags to ext. One side of every pair is the block's halves (queries, or
 // keys with SWAP), the other the step's chunk. All NT threads take part;
 // returns the steps left.
@@ -202,6 +202,7 @@ __device__ __forceinline__ int filter_steps(const Geom& g, const ModParams& m, i
       const Coord f = chunk_first(g, m, x, o);
       if (g.T - f.t < g.ct || g.H - f.h < g.ch || g.W - f.w < g.cw || g.cr < 64) x |= kEdge;
       if (k.ids.w) x |= kHidden;
+      if (f.t >= g.T || f.h >= g.H || f.w >= g.W) e = 0;  // a chunk of padding
     }
     const bool keep = (e >> 30) != 0;
     const uint32_t vote = __ballot_sync(0xffffffffu, keep);

@@ -104,6 +104,44 @@ __device__ __forceinline__ void compact_steps(const Geom& g, const uint32_t* bmA
   if (tid == 0) *count = (uint32_t)min(tot, cap);
 }
 
+// The same for mod::filter_steps, which looks at every entry anyway: chunks
+// of padding are listed too, and no coordinates are formed, so that a thread
+// only counts and writes. It takes the bitmaps by bytes: a dense list's words
+// would keep a few threads busy with 32 entries each.
+template <int NT>
+__device__ __forceinline__ void list_steps(const Geom& g, const uint32_t* bmA, const uint32_t* bmB, int words,
+                                           uint32_t* list, int cap, int* scan, uint32_t* count) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nb = 4 * words, per = (nb + NT - 1) / NT;
+  const int b0 = min(tid * per, nb), b1 = min(b0 + per, nb);
+  int mine = 0;
+  for (int q = b0; q < b1; ++q) mine += __popc(((bmA[q >> 2] | bmB[q >> 2]) >> (8 * (q & 3))) & 0xffu) * g.nchunk;
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  int pos = x - mine, tot = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    pos += i < warp ? scan[i] : 0;
+    tot += scan[i];
+  }
+  for (int q = b0; q < b1; ++q) {
+    const uint32_t a = (bmA[q >> 2] >> (8 * (q & 3))) & 0xffu, b = (bmB[q >> 2] >> (8 * (q & 3))) & 0xffu;
+    for (uint32_t bits = a | b; bits; bits &= bits - 1) {
+      const int bit = __ffs(bits) - 1;
+      const uint32_t e = (uint32_t)(8 * q + bit) | (((a >> bit) & 1u) << 30) | (((b >> bit) & 1u) << 31);
+      for (int c = 0; c < g.nchunk; ++c, ++pos)
+        if (pos < cap) list[pos] = e | ((uint32_t)c << 21);
+    }
+  }
+  if (tid == 0) *count = (uint32_t)min(tot, cap);
+}
+
 // Score rules: a chunk's row offsets, and every chunk's in-tile origin
 // (packed 10 bits per axis), so that a step needs no division.
 struct ModTab {

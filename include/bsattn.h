@@ -400,10 +400,11 @@ bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const 
  * in this order. Hidden pairs have probability 0; a query row that sees no
  * key gets O = 0 and lse = -inf, and no gradient reaches or leaves it. A
  * token with a negative id is hidden altogether: what its Q, K, V and dO
- * rows hold, NaN and infinities included, does not reach any other row.
- * Values at pairs that only `causal` or two different ids hide must be
- * finite. A sequence is a grid of one column (T = length, H = W = 1, tiles
- * of (64, 1, 1)). */
+ * rows hold, NaN and infinities included, does not reach any other row (tile
+ * scales of the e4m3 path must be finite; attn_layer_mod makes them without
+ * such tokens). Values at pairs that only `causal` or two different ids hide
+ * must be finite. A sequence is a grid of one column (T = length, H = W = 1,
+ * tiles of (64, 1, 1)). */
 typedef struct {
   float softcap;                 /* 0: off; else in [1e-6, 1e30]              */
   float dist_t, dist_h, dist_w;  /* >= 0, finite                              */
