@@ -176,7 +176,10 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   const Geom& g = P.g;
   const ModParams& M = P.mod;
-  const int item = blockIdx.x / P.parts, part = blockIdx.x % P.parts;
+  // Causal order: the last frames see the most keys, so they start first and
+  // the short lists fill the end of the grid.
+  const int first = M.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int item = first / P.parts, part = first % P.parts;
   int i0, i1, c0, c1;
   if (!work_halves<NAT>(P, item, &i0, &i1, &c0, &c1)) return;  // uniform over the CTA, before any set-up
   const int head = blockIdx.y, b = blockIdx.z;

@@ -176,7 +176,11 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
   const Geom& g = P.g;
   int i0, i1, c0 = 0, c1 = 0;
-  block_halves(g, P.pair_axis, P.pdim, blockIdx.x, &i0, &i1, &c0, &c1);
+  int item = blockIdx.x;
+  if constexpr (MOD) {  // causal order: the longest lists first, as in the forward
+    if (P.mod.causal) item = gridDim.x - 1 - blockIdx.x;
+  }
+  block_halves(g, P.pair_axis, P.pdim, item, &i0, &i1, &c0, &c1);
   const int head = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * g.Hh + head;
   const bool has1 = i1 >= 0;
