@@ -59,6 +59,7 @@ constexpr long long kTestWaitLimit = 2000000LL;  // ~1 ms, with the testing hook
 constexpr float kAbove = 40.f, kRaise = 30.f;
 constexpr float kSumLimit = 0x1p30f;  // no term of a smaller sum exceeds m + kRaise
 constexpr float kAboveUnit = 0x1p40f;
+constexpr float kLeastUnit = 1e-30f;
 
 struct Params {
   Geom g;
@@ -443,7 +444,12 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // bias is added in the same units, and one FMA per score applies
     // c = unit log2(e). `kq` takes raw products to the argument of tanh.
     const float slope = BIAS ? __ldg(M.slopes + head) : 0.f;
-    const float sq = P.scale * qsc, kq = sq / cap;
+    // e4m3 tiles of tiny values: a unit below kLeastUnit, whose scores (448^2 D
+    // units at most) are no more than 1e-22, is taken for it, so that the bias
+    // stays finite in it.
+    constexpr bool kFloor = FP8 && BIAS && !CAP;
+    const float sq = kFloor ? fmaxf(P.scale * qsc, kLeastUnit) : P.scale * qsc, kq = sq / cap;
+    const float least_ks = kFloor ? kLeastUnit / sq : 0.f;
     const float c_fix = (CAP ? cap : sq) * mod::kLog2e;     // c, without the key tile's scale
     const float nslope = -slope / (CAP ? cap : sq);         // likewise
     float m = -INFINITY, l = 0.f;
@@ -481,7 +487,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mod::Dist dist{};
       if (BIAS || (ext & mod::kSpecial)) {
         const mod::Coord f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
-        if (BIAS) dist = mod::make_dist(g, M, row.at, f, FP8 && !CAP ? nslope / uks[n] : nslope);
+        if (BIAS) dist = mod::make_dist(g, M, row.at, f, kFloor ? nslope / fmaxf(uks[n], least_ks) : nslope);
         if (ext & mod::kSpecial) {
           if ((ext & mod::kHidden) && warp < 2) {
             // V rows of hidden tokens become zeros before the product reads them.
@@ -502,7 +508,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
       }
-      const float ksc = FP8 ? uks[n] : 1.f;
+      const float ksc = kFloor ? fmaxf(uks[n], least_ks) : FP8 ? uks[n] : 1.f;
       const int n1 = min(n + 1, L - 1);
       e = ulist[n1];
       ext = uext[n1];

@@ -340,7 +340,7 @@ bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r) {
     sum += r->dim[a];
   }
   if (sum < 2 || sum > p->desc.head_dim) return BSATTN_ERR_INVALID_ARG;
-  if (!(r->base > 1.0) || !isfinite(r->base) || !isfinite(r->amplitude)) return BSATTN_ERR_INVALID_ARG;
+  if (!(r->base > 1.0) || !isfinite(r->base) || !isfinite((float)r->amplitude)) return BSATTN_ERR_INVALID_ARG;
   if (r->scaling != BSATTN_ROPE_SCALE_NONE)
     for (int a = 0; a < 3; ++a)
       if (!(r->factor[a] > 0.0) || !isfinite(r->factor[a])) return BSATTN_ERR_INVALID_ARG;
@@ -390,7 +390,8 @@ bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv
           keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
           f *= keep + (1.0 - keep) / s;
         }
-        const double turn = f / kTwoPi;  // below 2^63 in any use; the fraction is exact in 2^-64
+        const double turn = f / kTwoPi;
+        if (!isfinite(turn)) return BSATTN_ERR_INVALID_ARG;  // extreme factors
         prm.turns[np++] = fraction64(turn);
       }
     }

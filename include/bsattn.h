@@ -373,7 +373,7 @@ typedef struct {
   double factor[3];    /* s of each axis: > 0, finite (unused: NONE)          */
   double original[3];  /* BY_PARTS: original extent of each axis, > 0         */
   double slow, fast;   /* BY_PARTS: 0 <= slow < fast                          */
-  double amplitude;    /* finite; 0 selects 1                                 */
+  double amplitude;    /* finite in fp32; 0 selects 1                         */
   int offset[3];       /* added to the token's grid coordinates (pos NULL)    */
   const int32_t* pos;  /* NULL, or device [B, L, 3] positions (t, h, w) of
                           every token in place of grid coordinates            */
@@ -385,7 +385,8 @@ typedef struct {
  * gradient of x. pooled0/pooled1, if non-NULL, get the fp32 tile means of the
  * rotated values over real tokens, [B, Hh, N, D], as attn_pool gives them for
  * unrotated ones (taken before the rounding to bf16). INVALID_ARG: a field
- * outside its range, pointers as everywhere, pooled1 without x1. */
+ * outside its range, a frequency that is not finite in fp64, pointers as
+ * everywhere, pooled1 without x1. */
 bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const void* x0, void* y0,
                         const void* x1, void* y1, float* pooled0, float* pooled1, int transpose,
                         void* stream);
@@ -401,8 +402,8 @@ bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const 
  * key gets O = 0 and lse = -inf, and no gradient reaches or leaves it. A
  * token with a negative id is hidden altogether: what its Q, K, V and dO
  * rows hold, NaN and infinities included, does not reach any other row (tile
- * scales of the e4m3 path must be finite; attn_layer_mod makes them without
- * such tokens). Values at pairs that only `causal` or two different ids hide
+ * scales of the e4m3 path must be positive and finite, as attn_quantize_e4m3
+ * makes them of finite values; attn_layer_mod makes them without such tokens). Values at pairs that only `causal` or two different ids hide
  * must be finite. A sequence is a grid of one column (T = length, H = W = 1,
  * tiles of (64, 1, 1)). */
 typedef struct {

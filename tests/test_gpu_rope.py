@@ -163,6 +163,22 @@ def test_bad_descriptions_are_refused(bs, kw):
     assert e.value.code == 1
 
 
+@pytest.mark.parametrize("kw", [
+    dict(dims=(8, 8, 8), scaling="ntk", factor=(1.0, 1e300, 1.0)), dict(dims=(8, 8, 8), amplitude=1e39),
+    dict(dims=(8, 8, 8), scaling="linear", factor=(1e-310, 1.0, 1.0)),
+    dict(dims=(8, 8, 8), scaling="by_parts", original=(9.0, 9.0, 9.0), slow=4.0, fast=8.0, factor=(1.0, 1.0, 1e-310)),
+])
+def test_frequencies_without_a_value_are_refused(bs, kw):
+    plan = bs.Plan(1, 1, 128, 2, 2, 2, rule="window")
+    x = torch.zeros(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_rope(plan, bs.Rope(**kw), x, x)
+    assert e.value.code == 1
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_layer_mod(plan, bs.Rope(**kw), None, x, x, x, torch.empty_like(x), plan.workspace("mod_layer"))
+    assert e.value.code == 1
+
+
 def test_bad_tensors_are_refused(bs):
     plan = bs.Plan(1, 1, 64, 2, 2, 2, rule="window")
     x = torch.zeros(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")

@@ -300,6 +300,24 @@ def test_forward_e4m3(bs, grid, rule):
     assert torch.equal(back, o)
 
 
+@pytest.mark.parametrize("rule", ["bias", "all"])
+def test_e4m3_tiles_of_tiny_values(bs, rule):
+    """Scales whose product is no fp32 number: the scores are zero, the rest of the rules holds."""
+    c = Case(bs, "ragged", rule, seed=5, fp8=True)
+    plan, ws = c.plan, c.plan.workspace("mod_forward")
+    codes, scales = [], []
+    for x, tiny in ((c.q, 1e-36), (c.k, 1e-25)):
+        code, scale = e4m3.quantize_tiled(tiling.reorder(x.float().numpy(), *c.grid, c.tile))
+        codes.append(torch.from_numpy(code).cuda())
+        scales.append((torch.from_numpy(scale) * tiny).cuda())
+    o, lse = _nan(plan.natural_shape()), _nan((c.B, c.heads, c.L), torch.float32)
+    bs.attn_forward_natural_mod(plan, c.mod, *codes, c.v.cuda(), c.idx, c.cnt, o, ws, lse_nat=lse, q_scale=scales[0],
+                                k_scale=scales[1])
+    assert bs.attn_check_device_status(plan) == 0
+    zero = np.zeros(plan.natural_shape())
+    c.check_forward(to64(o), to64(lse), zero, zero, to64(c.v))
+
+
 # ---------------------------------------------------------------- routing
 
 def _tile_lists(c):
