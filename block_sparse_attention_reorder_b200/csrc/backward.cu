@@ -98,7 +98,7 @@ bsattn_status run_backward(const bsattn_plan* p, const __nv_bfloat16* q, const _
                            const __nv_bfloat16* v, const __nv_bfloat16* o, const __nv_bfloat16* d_o, const float* lse,
                            const int32_t* idx, const int32_t* cnt, __nv_bfloat16* dq, __nv_bfloat16* dk,
                            __nv_bfloat16* dv, const BackwardWs& w, cudaStream_t st, const ModParams* mod,
-                           float* neg_lse2, float* slope_parts) {
+                           float* neg_lse2, float* slope_parts, void* shares) {
   const Geom g = make_geom(p);
   const size_t rows = (size_t)g.B * g.Hh * g.N;  // tile rows of the lists
   const int words = (g.N + 31) / 32;
@@ -110,9 +110,10 @@ bsattn_status run_backward(const bsattn_plan* p, const __nv_bfloat16* q, const _
   if (cudaGetLastError() != cudaSuccess) return BSATTN_ERR_CUDA;
   // With score rules dQ comes first: it corrects Delta for dK.
   bsattn_status s = BSATTN_OK;
-  if (mod && (s = launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st, mod, neg_lse2, slope_parts)))
+  if (mod && (s = launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st, mod, neg_lse2, slope_parts,
+                                        shares)))
     return s;
-  s = launch_backward_dkdv_tc(p, q, k, v, d_o, mod ? neg_lse2 : lse, w.delta, w.idxT, w.cntT, dk, dv, st, mod);
+  s = launch_backward_dkdv_tc(p, q, k, v, d_o, mod ? neg_lse2 : lse, w.delta, w.idxT, w.cntT, dk, dv, st, mod, shares);
   if (s || mod) return s;
   return launch_backward_dq_tc(p, q, k, v, d_o, lse, w.delta, idx, cnt, dq, st);
 }
@@ -122,11 +123,11 @@ bsattn_status run_backward(const bsattn_plan* p, const __nv_bfloat16* q, const _
 bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* o,
                               const void* d_o, const float* lse, const int32_t* idx, const int32_t* cnt, void* dq,
                               void* dk, void* dv, const BackwardWs& w, cudaStream_t st, const ModParams* mod,
-                              float* neg_lse2, float* slope_parts) {
+                              float* neg_lse2, float* slope_parts, void* shares) {
   using B16 = __nv_bfloat16;
   if (p->desc.head_dim == 128)
     return run_backward<128>(p, (const B16*)q, (const B16*)k, (const B16*)v, (const B16*)o, (const B16*)d_o, lse,
-                             idx, cnt, (B16*)dq, (B16*)dk, (B16*)dv, w, st, mod, neg_lse2, slope_parts);
+                             idx, cnt, (B16*)dq, (B16*)dk, (B16*)dv, w, st, mod, neg_lse2, slope_parts, shares);
   return run_backward<64>(p, (const B16*)q, (const B16*)k, (const B16*)v, (const B16*)o, (const B16*)d_o, lse, idx,
-                          cnt, (B16*)dq, (B16*)dk, (B16*)dv, w, st, mod, neg_lse2, slope_parts);
+                          cnt, (B16*)dq, (B16*)dk, (B16*)dv, w, st, mod, neg_lse2, slope_parts, shares);
 }

@@ -70,6 +70,24 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128, kColOp = 192, kColDQ = 256, kColG = 384;
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles (~2 s)
 
+// A CTA's share of an accumulator row (fp32, the columns of half `part`), zeros
+// where the row is no visible token or nothing was summed.
+template <int D>
+__device__ __forceinline__ void store_share(float* dst, uint32_t src, int part, bool summed, bool live) {
+#pragma unroll
+  for (int col = part * (D / 2); col < (part + 1) * (D / 2); col += 32) {
+    uint32_t o[32];
+    if (summed) tc::tmem_ld32_wait(src + col, o);
+    if (!summed || !live) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q) o[q] = 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      reinterpret_cast<uint4*>(dst + col)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+  }
+}
+
 // Row r of a 128-row block in shared memory (128-byte swizzled 64-column
 // blocks of 16 KB) as an A operand in TMEM, two bf16 a column: the half that
 // `part` names, by the warps that own the row's lanes.
@@ -112,7 +130,10 @@ struct DqParamsMod : DqParams {
   ModParams mod;
   float* neg_delta;    // gets -(Delta + eps) of every row, 0 where no gradient passes
   float* neg_lse2;     // gets -lse log2(e) of every row, -inf where no gradient passes
-  float* slope_parts;  // null, or [B * heads, CTAs per head]: the slope gradient's parts
+  float* slope_parts;  // null, or [B * heads, backward_slope_items]: the slope gradient's parts
+  int shares;          // CTAs that share a query block's steps
+  float* part_q;       // shares > 1: [blocks, shares, 2, 128, D] dQ and G
+  float4* part_s;      // [blocks, shares, 128] (sum w, sum w dist, sum P dist, -Delta) of each row
 };
 
 template <int D, bool MOD, int kStages>
@@ -176,9 +197,11 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
   const Geom& g = P.g;
   int i0, i1, c0 = 0, c1 = 0;
-  int item = blockIdx.x;
+  int item = blockIdx.x, share = 0;
   if constexpr (MOD) {  // causal order: the longest lists first, as in the forward
     if (P.mod.causal) item = gridDim.x - 1 - blockIdx.x;
+    share = item % P.shares;
+    item /= P.shares;
   }
   block_halves(g, P.pair_axis, P.pdim, item, &i0, &i1, &c0, &c1);
   const int head = blockIdx.y, b = blockIdx.z;
@@ -270,7 +293,15 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  if constexpr (MOD) {
+    if (P.shares > 1) {  // this CTA's share of the steps
+      const int lo = L * share / P.shares;
+      L = L * (share + 1) / P.shares - lo;
+      ulist += lo;
+      uext += lo;
+    }
+  }
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {
@@ -586,64 +617,81 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float v = 0.f;
       const int o = 3 * (tid ^ 128);
       if (use && row.live) eps = sw + red[o];
-      if (part == 0 && row_exists) {
+      if (P.shares > 1) {
+        // The block's sums are complete only where its shares are joined.
+        const size_t at = ((bh * (gridDim.x / P.shares) + item) * P.shares + share) * 128 + r;
+        if (part == 0) {
+          P.part_s[at] = use && row.live ? make_float4(eps, swd + red[o + 1], spd + red[o + 2], ndlt)
+                                         : make_float4(0.f, 0.f, 0.f, ndlt);
+          if (share == 0 && row_exists) P.neg_lse2[lrow] = nlse2;
+        }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          float* dst = P.part_q + (((at - r) * 2 + which * 128) + r) * D;
+          store_share<D>(dst, tmem + lane_base + (which ? kColG : kColDQ), part, ok && L > 0, row.live);
+        }
+      } else if (part == 0 && row_exists) {
         P.neg_delta[lrow] = ndlt - eps;
         P.neg_lse2[lrow] = nlse2;
         if (use && row.live) v = eps * (spd + red[o + 2]) - (swd + red[o + 1]);
       }
-      if (P.slope_parts) {
+      if (P.slope_parts && P.shares == 1) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (part == 0 && lane == 0) scan[warp] = __float_as_int(v);
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
         if (tid == 0)
-          P.slope_parts[bh * gridDim.x + blockIdx.x] = (__int_as_float(scan[0]) + __int_as_float(scan[1])) +
+          P.slope_parts[bh * gridDim.x + item] = (__int_as_float(scan[0]) + __int_as_float(scan[1])) +
                                                        (__int_as_float(scan[2]) + __int_as_float(scan[3]));
       }
     }
-    uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
-    constexpr int OC = D / 2;  // dQ columns this warp writes
+    bool whole = true;
+    if constexpr (MOD) whole = P.shares == 1;
+    if (whole) {
+      uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
+      constexpr int OC = D / 2;  // dQ columns this warp writes
 #pragma unroll
-    for (int col = part * OC; col < part * OC + OC; col += 32) {
-      uint32_t o[32];
-      if (ok && L > 0) {
-        tc::tmem_ld32_wait(tmem + lane_base + kColDQ + col, o);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 32; ++q) o[q] = 0u;
-      }
-      if constexpr (MOD) {
+      for (int col = part * OC; col < part * OC + OC; col += 32) {
+        uint32_t o[32];
         if (ok && L > 0) {
-          uint32_t gr[32];
-          tc::tmem_ld32_wait(tmem + lane_base + kColG + col, gr);
-#pragma unroll
-          for (int q = 0; q < 32; ++q)
-            o[q] = __float_as_uint(fmaf(-eps, __uint_as_float(gr[q]), __uint_as_float(o[q])));
-        }
-        if (!row.live) {
+          tc::tmem_ld32_wait(tmem + lane_base + kColDQ + col, o);
+        } else {
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = 0u;
         }
-      }
-      uint32_t w[16];
+        if constexpr (MOD) {
+          if (ok && L > 0) {
+            uint32_t gr[32];
+            tc::tmem_ld32_wait(tmem + lane_base + kColG + col, gr);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(o[2 * q]) * P.scale,
-                                                  __uint_as_float(o[2 * q + 1]) * P.scale);
-        w[q] = *reinterpret_cast<uint32_t*>(&hv);
-      }
+            for (int q = 0; q < 32; ++q)
+              o[q] = __float_as_uint(fmaf(-eps, __uint_as_float(gr[q]), __uint_as_float(o[q])));
+          }
+          if (!row.live) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-    constexpr int CPR = D / 8;
-    const int rows = has1 ? 128 : 64;
-    for (int e2 = tid; e2 < rows * CPR; e2 += kSoftmaxThreads) {
-      const int rr = e2 / CPR, cc = e2 % CPR;
-      const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_K + rr * C::O_PITCH + cc * 16);
-      uint4* og = reinterpret_cast<uint4*>(P.dq + (size_t)(rr >> 6 ? tile_row(i1, c1) : tile_row(i0, c0)) * D);
-      og[(rr & 63) * CPR + cc] = val;
+            for (int q = 0; q < 32; ++q) o[q] = 0u;
+          }
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(o[2 * q]) * P.scale,
+                                                    __uint_as_float(o[2 * q + 1]) * P.scale);
+          w[q] = *reinterpret_cast<uint32_t*>(&hv);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+      constexpr int CPR = D / 8;
+      const int rows = has1 ? 128 : 64;
+      for (int e2 = tid; e2 < rows * CPR; e2 += kSoftmaxThreads) {
+        const int rr = e2 / CPR, cc = e2 % CPR;
+        const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_K + rr * C::O_PITCH + cc * 16);
+        uint4* og = reinterpret_cast<uint4*>(P.dq + (size_t)(rr >> 6 ? tile_row(i1, c1) : tile_row(i0, c0)) * D);
+        og[(rr & 63) * CPR + cc] = val;
+      }
     }
   }
 
@@ -653,6 +701,67 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (warp == 9) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the shares of each query block (small grids): eps = sum of the shares'
+// eps, dQ = scale (sum dQ - eps sum G), and each CTA's part of the slope
+// gradient. D / 8 threads a row, eight features each, kJoinRows rows a CTA,
+// every load of a thread in flight at once; sums in the order of the shares.
+constexpr int kMaxShares = 8, kJoinRows = 16, kJoinBlocks = 128 / kJoinRows;
+__device__ __forceinline__ void add8(float* s, const float* src) {
+  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+  s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+  s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+}
+__device__ __forceinline__ uint4 pack8(const float* s, float mul) {
+  return make_uint4(mod::pack(make_float2(s[0] * mul, s[1] * mul)), mod::pack(make_float2(s[2] * mul, s[3] * mul)),
+                    mod::pack(make_float2(s[4] * mul, s[5] * mul)), mod::pack(make_float2(s[6] * mul, s[7] * mul)));
+}
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * D / 8) bwd_dq_join_kernel(const __grid_constant__ DqParamsMod P) {
+  __shared__ float sums[kJoinRows];
+  const Geom& g = P.g;
+  const int item = blockIdx.x / kJoinBlocks, items = gridDim.x / kJoinBlocks, piece = threadIdx.x % (D / 8);
+  const int r = blockIdx.x % kJoinBlocks * kJoinRows + threadIdx.x / (D / 8), half = r >> 6;
+  const size_t bh = (size_t)blockIdx.z * g.Hh + blockIdx.y;
+  int i0, i1, c0 = 0, c1 = 0;
+  block_halves(g, P.pair_axis, P.pdim, item, &i0, &i1, &c0, &c1);
+  float v = 0.f;
+  if (half == 0 || i1 >= 0) {
+    const size_t at = (bh * items + item) * P.shares;
+    float4 s[kMaxShares];
+    float dq[8] = {}, gr[8] = {};
+#pragma unroll
+    for (int p = 0; p < kMaxShares; ++p) {
+      if (p >= P.shares) continue;
+      s[p] = P.part_s[(at + p) * 128 + r];
+      const float* src = P.part_q + ((at + p) * 256 + r) * D + 8 * piece;
+      add8(dq, src);
+      add8(gr, src + 128 * D);
+    }
+    float eps = 0.f, wd = 0.f, pd = 0.f;
+#pragma unroll
+    for (int p = 0; p < kMaxShares; ++p) {
+      if (p >= P.shares) continue;
+      eps += s[p].x;
+      wd += s[p].y;
+      pd += s[p].z;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dq[q] = fmaf(-eps, gr[q], dq[q]);
+    const size_t row = (bh * g.N + (half ? i1 : i0)) * g.V + 64 * (half ? c1 : c0) + (r & 63);
+    reinterpret_cast<uint4*>(P.dq + row * D)[piece] = pack8(dq, P.scale);
+    if (piece == 0) P.neg_delta[row] = s[0].w - eps;
+    v = eps * pd - wd;
+  }
+  if (!P.slope_parts) return;
+  if (piece == 0) sums[threadIdx.x / (D / 8)] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f;
+    for (int i = 0; i < kJoinRows; ++i) t += sums[i];
+    P.slope_parts[bh * gridDim.x + blockIdx.x] = t;
   }
 }
 
@@ -674,9 +783,14 @@ bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const v
   auto kern = bwd_dq_tc_kernel<D, MOD, kStages>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
+  const int items = attention_items(p);
   dim3 grid(items, p->desc.heads, p->desc.B);
+  if constexpr (MOD) grid.x *= prm.shares;
   kern<<<grid, kThreads, smem, st>>>(mq, mdo, mk, mv, prm);
+  if constexpr (MOD) {
+    if (prm.shares > 1)
+      bwd_dq_join_kernel<D><<<dim3(items * kJoinBlocks, p->desc.heads, p->desc.B), kJoinRows * D / 8, 0, st>>>(prm);
+  }
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
@@ -711,6 +825,8 @@ struct KvParams {
 
 struct KvParamsMod : KvParams {
   ModParams mod;
+  int shares;          // CTAs that share a key block's steps
+  float* part_kv;      // shares > 1: [blocks, shares, 2, 128, D] dK (not yet scaled) and dV
 };
 
 template <int D, bool MOD, int kStages>
@@ -776,7 +892,12 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   const Geom& g = P.g;
   int j0, j1, kc0 = 0, kc1 = 0;
-  block_halves(g, P.pair_axis, P.pdim, blockIdx.x, &j0, &j1, &kc0, &kc1);
+  int item = blockIdx.x, share = 0;
+  if constexpr (MOD) {
+    share = item % P.shares;
+    item /= P.shares;
+  }
+  block_halves(g, P.pair_axis, P.pdim, item, &j0, &j1, &kc0, &kc1);
   const int head = blockIdx.y, b = blockIdx.z;
   const size_t bh = (size_t)b * g.Hh + head;
   const bool has1 = j1 >= 0;
@@ -865,7 +986,15 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
+  if constexpr (MOD) {
+    if (P.shares > 1) {  // this CTA's share of the steps
+      const int lo = L * share / P.shares;
+      L = L * (share + 1) / P.shares - lo;
+      ulist += lo;
+      uext += lo;
+    }
+  }
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {
@@ -1167,49 +1296,60 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       tc::fence_after_sync();
     }
-    // dK (scaled) and dV rows staged in the ring: dK at rows 0-127, dV at 128-255.
-    constexpr int OC = D / 2;
+    bool whole = true;
+    if constexpr (MOD) {
+      whole = P.shares == 1;
+      if (!whole) {
+        float* dst = P.part_kv + (((bh * (gridDim.x / P.shares) + item) * P.shares + share) * 2 * 128 + r) * D;
+        store_share<D>(dst, tmem + lane_base + kColDK, part, ok && L > 0, row.live);
+        store_share<D>(dst + 128 * D, tmem + lane_base + kColDV, part, ok && L > 0, row.live);
+      }
+    }
+    if (whole) {
+      // dK (scaled) and dV rows staged in the ring: dK at rows 0-127, dV at 128-255.
+      constexpr int OC = D / 2;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      uint8_t* stage = smem + C::OFF_RING + (which * 128 + r) * C::O_PITCH;
-      const float mul = which == 0 ? P.scale : 1.f;
-      const uint32_t base = which == 0 ? kColDK : kColDV;
+      for (int which = 0; which < 2; ++which) {
+        uint8_t* stage = smem + C::OFF_RING + (which * 128 + r) * C::O_PITCH;
+        const float mul = which == 0 ? P.scale : 1.f;
+        const uint32_t base = which == 0 ? kColDK : kColDV;
 #pragma unroll
-      for (int col = part * OC; col < part * OC + OC; col += 32) {
-        uint32_t o[32];
-        if (ok && L > 0) {
-          tc::tmem_ld32_wait(tmem + lane_base + base + col, o);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = 0u;
-        }
-        if constexpr (MOD) {
-          if (!row.live) {
+        for (int col = part * OC; col < part * OC + OC; col += 32) {
+          uint32_t o[32];
+          if (ok && L > 0) {
+            tc::tmem_ld32_wait(tmem + lane_base + base + col, o);
+          } else {
 #pragma unroll
             for (int q = 0; q < 32; ++q) o[q] = 0u;
           }
-        }
-        uint32_t w[16];
+          if constexpr (MOD) {
+            if (!row.live) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(o[2 * q]) * mul, __uint_as_float(o[2 * q + 1]) * mul);
-          w[q] = *reinterpret_cast<uint32_t*>(&hv);
-        }
+              for (int q = 0; q < 32; ++q) o[q] = 0u;
+            }
+          }
+          uint32_t w[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          for (int q = 0; q < 16; ++q) {
+            __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(o[2 * q]) * mul, __uint_as_float(o[2 * q + 1]) * mul);
+            w[q] = *reinterpret_cast<uint32_t*>(&hv);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            reinterpret_cast<uint4*>(stage + col * 2)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
       }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-    constexpr int CPR = D / 8;
-    const int rows = has1 ? 128 : 64;
-    for (int e2 = tid; e2 < 2 * rows * CPR; e2 += kSoftmaxThreads) {
-      const int which = e2 / (rows * CPR), rem = e2 % (rows * CPR);
-      const int rr = rem / CPR, cc = rem % CPR;
-      const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_RING + (which * 128 + rr) * C::O_PITCH + cc * 16);
-      __nv_bfloat16* dst = which == 0 ? P.dk : P.dv;
-      uint4* og = reinterpret_cast<uint4*>(dst + (size_t)(rr >> 6 ? tile_row(j1, kc1) : tile_row(j0, kc0)) * D);
-      og[(rr & 63) * CPR + cc] = val;
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+      constexpr int CPR = D / 8;
+      const int rows = has1 ? 128 : 64;
+      for (int e2 = tid; e2 < 2 * rows * CPR; e2 += kSoftmaxThreads) {
+        const int which = e2 / (rows * CPR), rem = e2 % (rows * CPR);
+        const int rr = rem / CPR, cc = rem % CPR;
+        const uint4 val = *reinterpret_cast<const uint4*>(smem + C::OFF_RING + (which * 128 + rr) * C::O_PITCH + cc * 16);
+        __nv_bfloat16* dst = which == 0 ? P.dk : P.dv;
+        uint4* og = reinterpret_cast<uint4*>(dst + (size_t)(rr >> 6 ? tile_row(j1, kc1) : tile_row(j0, kc0)) * D);
+        og[(rr & 63) * CPR + cc] = val;
+      }
     }
   }
 
@@ -1220,6 +1360,30 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Joins the shares of each key block, as bwd_dq_join_kernel.
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * D / 8) bwd_dkdv_join_kernel(const __grid_constant__ KvParamsMod P) {
+  const Geom& g = P.g;
+  const int item = blockIdx.x / kJoinBlocks, items = gridDim.x / kJoinBlocks, piece = threadIdx.x % (D / 8);
+  const int r = blockIdx.x % kJoinBlocks * kJoinRows + threadIdx.x / (D / 8), half = r >> 6;
+  const size_t bh = (size_t)blockIdx.z * g.Hh + blockIdx.y;
+  int j0, j1, c0 = 0, c1 = 0;
+  block_halves(g, P.pair_axis, P.pdim, item, &j0, &j1, &c0, &c1);
+  if (half && j1 < 0) return;
+  const size_t at = (bh * items + item) * P.shares;
+  float dk[8] = {}, dv[8] = {};
+#pragma unroll
+  for (int p = 0; p < kMaxShares; ++p) {
+    if (p >= P.shares) continue;
+    const float* src = P.part_kv + ((at + p) * 256 + r) * D + 8 * piece;
+    add8(dk, src);
+    add8(dv, src + 128 * D);
+  }
+  const size_t row = (bh * g.N + (half ? j1 : j0)) * g.V + 64 * (half ? c1 : c0) + (r & 63);
+  reinterpret_cast<uint4*>(P.dk + row * D)[piece] = pack8(dk, P.scale);
+  reinterpret_cast<uint4*>(P.dv + row * D)[piece] = pack8(dv, 1.f);
 }
 
 template <int D, bool MOD, int kStages>
@@ -1240,9 +1404,14 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
   auto kern = bwd_dkdv_tc_kernel<D, MOD, kStages>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
-  const int items = p->nchunk > 1 ? p->N * ((p->nchunk + 1) / 2) : prm.pdim[0] * prm.pdim[1] * prm.pdim[2];
+  const int items = attention_items(p);
   dim3 grid(items, p->desc.heads, p->desc.B);
+  if constexpr (MOD) grid.x *= prm.shares;
   kern<<<grid, kThreads, smem, st>>>(mq, mdo, mk, mv, prm);
+  if constexpr (MOD) {
+    if (prm.shares > 1)
+      bwd_dkdv_join_kernel<D><<<dim3(items * kJoinBlocks, p->desc.heads, p->desc.B), kJoinRows * D / 8, 0, st>>>(prm);
+  }
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
@@ -1262,10 +1431,43 @@ static bool fits(const P& prm) {
   return smem_of<C>(prm) <= 227 * 1024;
 }
 
+// Most steps a block may have: the union of two kept lists (one list for tiles
+// of several chunks) or, for key blocks, all query tiles, times the chunks.
+static int query_steps(const bsattn_plan* p) {
+  return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+}
+static int key_steps(const bsattn_plan* p) { return p->N * p->nchunk; }
+// Under score rules, on grids that leave half of the SMs or more idle, up to
+// eight CTAs share a block's steps, one per SM over the grid and four steps
+// each at least, and a second kernel joins their sums. A step takes 1.2 us
+// there and the join 6 to 8, so the shares must save eight steps. On one B200
+// with cap and bias (all launches of a backward): 2,048 tokens of one head 127
+// us alone, 70 shared; two heads of 8 x 16 x 16 tokens in a (3,3,3) window 80
+// and 55; 18 (6,8,8) tiles of one head 174 and 81.
+static int backward_shares(const bsattn_plan* p, int steps) {
+  const long long blocks = (long long)attention_items(p) * p->desc.heads * p->desc.B;
+  long long n = 148 / blocks;
+  if (n > steps / 4) n = steps / 4;
+  if (n > kMaxShares) n = kMaxShares;
+  return n < 2 || steps - steps / n < 8 ? 1 : (int)n;
+}
+static size_t share_rows(const bsattn_plan* p, int shares) {
+  return shares == 1 ? 0 : (size_t)attention_items(p) * p->desc.heads * p->desc.B * shares * 128;
+}
+size_t backward_mod_workspace_bytes(const bsattn_plan* p) {
+  const size_t d = p->desc.head_dim, nq = share_rows(p, backward_shares(p, query_steps(p))),
+               nk = share_rows(p, backward_shares(p, key_steps(p)));
+  const size_t a = nq * (2 * d * sizeof(float) + sizeof(float4)), b = nk * 2 * d * sizeof(float);
+  return a > b ? a : b;  // the passes follow one another
+}
+int backward_slope_items(const bsattn_plan* p) {
+  return attention_items(p) * (backward_shares(p, query_steps(p)) > 1 ? kJoinBlocks : 1);
+}
+
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod,
-                                    float* neg_lse2, float* slope_parts) {
+                                    float* neg_lse2, float* slope_parts, void* shares) {
   DqParamsMod prm;
   prm.g = make_geom(p);
   prm.idx = idx;
@@ -1277,8 +1479,7 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
   prm.scale = p->scale;
   prm.scale_log2 = p->scale * 1.4426950408889634f;
   prm.err = p->d_err;
-  // Steps: the union of two kept lists (one list for tiles of several chunks), times the chunks.
-  prm.umax = p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+  prm.umax = query_steps(p);
   prm.bm_words = (p->N + 31) / 32;
   prm.pair_axis = pair_axis_of(p);
   const int nd[3] = {p->nT, p->nH, p->nW};
@@ -1289,6 +1490,9 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
     prm.neg_delta = delta;
     prm.neg_lse2 = neg_lse2;
     prm.slope_parts = slope_parts;
+    prm.shares = backward_shares(p, prm.umax);
+    prm.part_q = (float*)shares;
+    prm.part_s = (float4*)(prm.part_q + share_rows(p, prm.shares) * 2 * p->desc.head_dim);
     if (d128)
       return fits<DqCfg<128, true, 4>>(prm) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)
                                             : run_dq<128, true, 3>(p, q, k, v, d_o, prm, st);
@@ -1301,7 +1505,7 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                       const void* d_o, const float* lse, const float* delta, const int32_t* idxT,
                                       const int32_t* cntT, void* dk, void* dv, cudaStream_t st,
-                                      const ModParams* mod) {
+                                      const ModParams* mod, void* shares) {
   KvParamsMod prm;
   prm.g = make_geom(p);
   prm.idxT = idxT;
@@ -1313,8 +1517,7 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
   prm.scale = p->scale;
   prm.scale_log2 = p->scale * 1.4426950408889634f;
   prm.err = p->d_err;
-  // Steps: at most N query tiles in the union of two transposed lists, times their chunks.
-  prm.umax = p->N * p->nchunk;
+  prm.umax = key_steps(p);
   prm.bm_words = (p->N + 31) / 32;
   prm.pair_axis = pair_axis_of(p);
   const int nd[3] = {p->nT, p->nH, p->nW};
@@ -1322,6 +1525,8 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
   const bool d128 = p->desc.head_dim == 128;
   if (mod) {
     prm.mod = *mod;
+    prm.shares = backward_shares(p, prm.umax);
+    prm.part_kv = (float*)shares;
     if (d128)
       return fits<KvCfg<128, true, 4>>(prm) ? run_dkdv<128, true, 4>(p, q, k, v, d_o, prm, st)
                                             : run_dkdv<128, true, 3>(p, q, k, v, d_o, prm, st);

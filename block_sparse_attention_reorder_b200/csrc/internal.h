@@ -216,7 +216,8 @@ struct BackwardWs {
 bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k, const void* v, const void* o,
                               const void* d_o, const float* lse, const int32_t* idx, const int32_t* cnt, void* dq,
                               void* dk, void* dv, const BackwardWs& w, cudaStream_t st,
-                              const ModParams* mod = nullptr, float* neg_lse2 = nullptr, float* slope_parts = nullptr);
+                              const ModParams* mod = nullptr, float* neg_lse2 = nullptr, float* slope_parts = nullptr,
+                              void* shares = nullptr);
 
 // dQ of the backward on the tensor cores (tiled bf16 q, k, v, dO; lse and
 // rowsum(dO * O) tiled fp32; with score rules delta becomes the negative of the corrected one, and
@@ -224,13 +225,17 @@ bsattn_status launch_backward(const bsattn_plan* p, const void* q, const void* k
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                     const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod = nullptr,
-                                    float* neg_lse2 = nullptr, float* slope_parts = nullptr);
+                                    float* neg_lse2 = nullptr, float* slope_parts = nullptr, void* shares = nullptr);
+// With score rules: scratch of both passes (`shares`), and the slope gradient's
+// parts per (batch, head).
+size_t backward_mod_workspace_bytes(const bsattn_plan* p);
+int backward_slope_items(const bsattn_plan* p);
 
 // dK and dV of the backward on the tensor cores, over the transposed lists.
 bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
                                       const void* d_o, const float* lse, const float* delta, const int32_t* idxT,
                                       const int32_t* cntT, void* dk, void* dv, cudaStream_t st,
-                                      const ModParams* mod = nullptr);
+                                      const ModParams* mod = nullptr, void* shares = nullptr);
 // CTAs of the attention kernels per (batch, head): 128-row query (key) blocks.
 static inline int attention_items(const bsattn_plan* p) {
   if (p->nchunk > 1) return p->N * ((p->nchunk + 1) / 2);

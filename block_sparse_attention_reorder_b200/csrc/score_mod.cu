@@ -39,14 +39,16 @@ struct BwdModWs {
   DocWs doc;
   float* slope_parts;
   float* neg_lse2;
+  void* shares;
   BackwardWs b;
 };
 BwdModWs carve_backward_mod(const bsattn_plan* p, Carve& c) {
   const size_t rows = (size_t)p->desc.B * p->desc.heads * p->N;
   BwdModWs w;
   w.doc = carve_doc(p, c);
-  w.slope_parts = (float*)c.take((size_t)p->desc.B * p->desc.heads * attention_items(p) * sizeof(float));
+  w.slope_parts = (float*)c.take((size_t)p->desc.B * p->desc.heads * backward_slope_items(p) * sizeof(float));
   w.neg_lse2 = (float*)c.take(rows * p->V * sizeof(float));
+  w.shares = c.take(backward_mod_workspace_bytes(p));
   w.b.delta = (float*)c.take(rows * p->V * sizeof(float));
   w.b.bm = (uint32_t*)c.take(rows * ((p->N + 31) / 32) * sizeof(uint32_t));
   w.b.idxT = (int32_t*)c.take(rows * p->N * sizeof(int32_t));
@@ -439,10 +441,11 @@ bsattn_status attn_backward_mod(const bsattn_plan* p, const bsattn_score_mod* m,
   if ((s = launch_doc_prep(p, m, w.doc, st))) return s;
   const ModParams d = device_mod(p, m, w.doc);
   if ((s = launch_backward(p, q, k, v, o, d_o, lse, idx, cnt, dq, dk, dv, w.b, st, &d, w.neg_lse2,
-                           d_slopes ? w.slope_parts : nullptr)))
+                           d_slopes ? w.slope_parts : nullptr, w.shares)))
     return s;
   if (!d_slopes) return BSATTN_OK;
-  slope_sum_kernel<<<p->desc.heads, 256, 0, st>>>(w.slope_parts, p->desc.B, p->desc.heads, attention_items(p), d_slopes);
+  slope_sum_kernel<<<p->desc.heads, 256, 0, st>>>(w.slope_parts, p->desc.B, p->desc.heads, backward_slope_items(p),
+                                                d_slopes);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 

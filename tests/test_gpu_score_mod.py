@@ -29,6 +29,7 @@ GRIDS = {  # B, heads, D, (T, H, W), tile, kept share (None: all tiles)
     "seq64": (2, 1, 128, (64, 1, 1), (64, 1, 1), None),
     "seq65": (1, 2, 128, (65, 1, 1), (64, 1, 1), None),
     "seq400": (2, 2, 128, (400, 1, 1), (64, 1, 1), None),
+    "seq2050": (1, 1, 128, (2050, 1, 1), (64, 1, 1), 0.6),
     "seq300_wide": (1, 2, 64, (300, 1, 1), (128, 1, 1), None),
 }
 RULES = {
