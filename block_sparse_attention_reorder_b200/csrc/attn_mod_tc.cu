@@ -269,21 +269,17 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   {
     const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, false>(g, M, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, false>(g, M, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
     __syncthreads();
+    if (BIAS) nearest_first<kThreads>(ulist, uext, left, i0);
+    if (P.parts > 1) left = take_share<kThreads>(ulist, uext, left, part, P.parts);
     if (tid == 0) misc[2] = (uint32_t)left;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
-  if (P.parts > 1) {  // this CTA's share of the steps
-    const int lo = L * part / P.parts;
-    L = L * (part + 1) / P.parts - lo;
-    ulist += lo;
-    uext += lo;
-  }
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 4) {

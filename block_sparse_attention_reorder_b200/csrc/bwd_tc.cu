@@ -285,23 +285,16 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
     __syncthreads();
+    if (P.shares > 1) left = take_share<kThreads>(ulist, uext, left, share, P.shares);
     if (tid == 0) misc[2] = (uint32_t)left;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
-  if constexpr (MOD) {
-    if (P.shares > 1) {  // this CTA's share of the steps
-      const int lo = L * share / P.shares;
-      L = L * (share + 1) / P.shares - lo;
-      ulist += lo;
-      uext += lo;
-    }
-  }
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {
@@ -978,23 +971,16 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    const int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, steps, scan);
     __syncthreads();
+    if (P.shares > 1) left = take_share<kThreads>(ulist, uext, left, share, P.shares);
     if (tid == 0) misc[2] = (uint32_t)left;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
-  if constexpr (MOD) {
-    if (P.shares > 1) {  // this CTA's share of the steps
-      const int lo = L * share / P.shares;
-      L = L * (share + 1) / P.shares - lo;
-      ulist += lo;
-      uext += lo;
-    }
-  }
+  const int L = __shfl_sync(0xffffffffu, (int)misc[2], 0);
 
   // ------------------------------------------------------------ roles
   if (warp == 8) {

@@ -142,6 +142,51 @@ __device__ __forceinline__ void list_steps(const Geom& g, const uint32_t* bmA, c
   if (tid == 0) *count = (uint32_t)min(tot, cap);
 }
 
+// Turns the first part of an ascending list, the steps up to the query tile,
+// around: a walk then starts at the query tile and leaves it in both
+// directions, so that under a distance bias the nearest keys come first and a
+// row's reference, set by its first keys, seldom has to move.
+template <int NT>
+__device__ __forceinline__ void nearest_first(uint32_t* list, uint32_t* ext, int steps, int tile) {
+  int lo = 0, hi = steps;  // steps of tiles <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if ((int)(list[mid] & 0x1FFFFFu) <= tile) lo = mid + 1;
+    else hi = mid;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < lo / 2; e += NT) {
+    const int f = lo - 1 - e;
+    const uint32_t a = list[e], x = ext[e];
+    list[e] = list[f];
+    ext[e] = ext[f];
+    list[f] = a;
+    ext[f] = x;
+  }
+  __syncthreads();
+}
+
+// Brings one of `shares` equal parts of the list to its front; returns its steps.
+template <int NT>
+__device__ __forceinline__ int take_share(uint32_t* list, uint32_t* ext, int steps, int share, int shares) {
+  const int lo = steps * share / shares, n = steps * (share + 1) / shares - lo;
+  for (int base = 0; lo > 0 && base < n; base += NT) {
+    const int i = base + threadIdx.x;
+    uint32_t e = 0, x = 0;
+    if (i < n) {
+      e = list[lo + i];
+      x = ext[lo + i];
+    }
+    __syncthreads();
+    if (i < n) {  // entries of later rounds lie behind this round's places
+      list[i] = e;
+      ext[i] = x;
+    }
+    __syncthreads();
+  }
+  return n;
+}
+
 // Score rules: a chunk's row offsets, and every chunk's in-tile origin
 // (packed 10 bits per axis), so that a step needs no division.
 struct ModTab {
