@@ -333,9 +333,10 @@ __device__ __forceinline__ void axis_distance(float* y, const float* d, float at
 }
 // In chunks whose rows of four or eight lie along w the t and h terms are one
 // value for four columns and the w terms four or eight values per step: three
-// operations a column. Chunks that are a line (sequences) take one where no
-// query of the warp stands among the columns (the distance is linear there: two
-// packed operations a pair), else two. Axis
+// operations a column. Chunks that are a line (sequences) take two; with all 64 columns
+// at a time one where no query of the warp stands among them (the distance is
+// linear there, two packed operations a pair: 8 x 16K tokens 1,300 -> 1,195 us;
+// beside the cap's 32 columns at a time the larger code costs 4%). Axis
 // after axis, seven with the table reads, serves the other shapes and passes
 // over axes of weight zero.
 template <int N, bool SET = false>
@@ -360,7 +361,7 @@ __device__ __forceinline__ void add_distance(const Geom& g, float* y, const Tabl
     const float at = g.ct == 64 ? p.t : p.w, n = g.ct == 64 ? p.nt : p.nw;
     const float u = fmaf(p.nh, fabsf(p.h), g.ct == 64 ? p.nw * fabsf(p.w) : p.nt * fabsf(p.t));
     const float a0 = at - (float)first;
-    if (__all_sync(0xffffffffu, a0 >= (float)(N - 1) || a0 <= 0.f)) {  // every row before or behind the columns
+    if (N == 64 && __all_sync(0xffffffffu, a0 >= (float)(N - 1) || a0 <= 0.f)) {  // every row before or behind the columns
       const float k = a0 <= 0.f ? n : -n;  // |a0 - q| n = k q - k a0
       const float2 k2 = bc(k), base = bc(fmaf(-k, a0, u));
 #pragma unroll
