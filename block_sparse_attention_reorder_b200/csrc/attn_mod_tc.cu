@@ -239,7 +239,35 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   const int prefix = M.prefix ? __ldg(M.prefix + b) : 0;
+  // A natural-layout load fills the chunk box's rows (cr of them).
+  const int qrows = NAT && !FP8 ? g.cr : 64, kvrows = NAT ? g.cr : 64;
+  // One chunk (64 tokens x 64 columns) of a natural-layout tensor: the
+  // box {64 columns, cw, ch, ct, 1} at the chunk's first token.
+  auto load_nat = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, mod::Coord p) {
+    tc::tma_load_5d(dst, map, bar, col, p.w, p.h, p.t, b);
+  };
+  if (warp == 4 && lane == 0) {
+    tc::tma_prefetch_desc(&tmQ);
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+  }
   __syncthreads();
+  if (warp == 4 && lane == 0) {  // the block's Q, while the list is made
+    tc::mbar_arrive_expect_tx(bar_q, (has1 ? 2 : 1) * qrows * C::QRB);
+    for (int x = 0; x < (has1 ? 2 : 1); ++x) {
+      const int tile = x ? i1 : i0, chunk = x ? c1 : c0;
+      const mod::Coord qp = mod::chunk_first(g, M, mod::pack_tile(g, M, tile), mod::origin_of(g, chunk));
+#pragma unroll
+      for (int cb = 0; cb < C::QBLK; ++cb) {
+        const uint32_t dst = sb + C::OFF_Q + cb * 128 * C::SWB + x * 64 * C::SWB;
+        if (NAT && !FP8)
+          load_nat(dst, &tmQ, bar_q, head * D + cb * 64, qp);
+        else
+          tc::tma_load_2d(dst, &tmQ, bar_q, cb * C::SWB / C::ESZ, tiled_row(tile, chunk));
+      }
+    }
+  }
+  __syncwarp();
   if (nA < 0 || nA > P.kmax || nB < 0 || nB > P.kmax) {
     if (tid == 0) atomicOr(P.err, BSATTN_DEVERR_BAD_INDEX);
     nA = min(max(nA, 0), P.kmax);
@@ -269,7 +297,8 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   {
     const int steps = (int)misc[2];
-    int left = mod::filter_steps<kThreads, false>(g, M, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, false>(g, M, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan,
+                                                       tab->origin);
     __syncthreads();
     if (BIAS) nearest_first<kThreads>(ulist, uext, left, i0);
     if (P.parts > 1) left = take_share<kThreads>(ulist, uext, left, part, P.parts);
@@ -284,29 +313,6 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // ------------------------------------------------------------ roles
   if (warp == 4) {
     if (lane == 0 && L > 0) {
-      tc::tma_prefetch_desc(&tmQ);
-      tc::tma_prefetch_desc(&tmK);
-      tc::tma_prefetch_desc(&tmV);
-      // A natural-layout load fills the chunk box's rows (cr of them).
-      const int qrows = NAT && !FP8 ? g.cr : 64, kvrows = NAT ? g.cr : 64;
-      // One chunk (64 tokens x 64 columns) of a natural-layout tensor: the
-      // box {64 columns, cw, ch, ct, 1} at the chunk's first token.
-      auto load_nat = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, mod::Coord p) {
-        tc::tma_load_5d(dst, map, bar, col, p.w, p.h, p.t, b);
-      };
-      tc::mbar_arrive_expect_tx(bar_q, (has1 ? 2 : 1) * qrows * C::QRB);
-      for (int x = 0; x < (has1 ? 2 : 1); ++x) {
-        const int tile = x ? i1 : i0, chunk = x ? c1 : c0;
-        const mod::Coord qp = mod::chunk_first(g, M, mod::pack_tile(g, M, tile), chunk_origin(g, chunk));
-#pragma unroll
-        for (int cb = 0; cb < C::QBLK; ++cb) {
-          const uint32_t dst = sb + C::OFF_Q + cb * 128 * C::SWB + x * 64 * C::SWB;
-          if (NAT && !FP8)
-            load_nat(dst, &tmQ, bar_q, head * D + cb * 64, qp);
-          else
-            tc::tma_load_2d(dst, &tmQ, bar_q, cb * C::SWB / C::ESZ, tiled_row(tile, chunk));
-        }
-      }
       // K_m is issued as soon as S_{m-2} has released its slot, V_{m-1} once
       // PV_{m-3} has: K runs one step ahead of V.
       int lastk[kStages], lastv[kStages];
@@ -356,13 +362,13 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       if (*abort_flag) {
         // Let copies already issued land before the CTA's memory goes away.
-        tc::mbar_wait(bar_q, 0, never, kWaitLimit);
         for (int s = 0; s < kStages; ++s) {
           if (lastk[s] >= 0) tc::mbar_wait(bar_kfull(s), (lastk[s] / kStages) & 1, never, kWaitLimit);
           if (lastv[s] >= 0) tc::mbar_wait(bar_vfull(s), (lastv[s] / kStages) & 1, never, kWaitLimit);
         }
       }
     }
+    if (lane == 0 && (L == 0 || *abort_flag)) tc::mbar_wait(bar_q, 0, never, kWaitLimit);  // the block's load too
   } else if (warp == 5) {
     if (L > 0) {
       const uint32_t lead = tc::elect_one();

@@ -285,7 +285,8 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, false>(g, P.mod, b, prefix, i0, i1, c0, c1, ulist, uext, steps, scan,
+                                                       tab->origin);
     __syncthreads();
     if (P.shares > 1) left = take_share<kThreads>(ulist, uext, left, share, P.shares);
     if (tid == 0) misc[2] = (uint32_t)left;
@@ -971,7 +972,8 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     fill_modtab<kThreads>(g, tab, colc);
     __syncthreads();
     const int steps = (int)misc[2];
-    int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, steps, scan);
+    int left = mod::filter_steps<kThreads, true>(g, P.mod, b, prefix, j0, j1, kc0, kc1, ulist, uext, steps, scan,
+                                                       tab->origin);
     __syncthreads();
     if (P.shares > 1) left = take_share<kThreads>(ulist, uext, left, share, P.shares);
     if (tid == 0) misc[2] = (uint32_t)left;

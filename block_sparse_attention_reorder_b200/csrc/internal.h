@@ -173,6 +173,7 @@ struct ModParams {
   const int32_t* doc_rows;   // null: no documents; [B, N, V] ids in tile order, padded slots -1
   const DocChunk* doc_chunks;  // [B, N, nchunk]
   int sh_h, sh_w;            // bits of a tile's h and w coordinates (packed step coordinates)
+  float per_plane, per_row;  // 1 / (nH nW), 1 / nW
 };
 
 // Where the attention's tensors live. Tiled: all tiled. Natural: Q, K, V, O

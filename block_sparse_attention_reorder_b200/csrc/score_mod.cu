@@ -312,6 +312,8 @@ ModParams device_mod(const bsattn_plan* p, const bsattn_score_mod* m, const DocW
   d.doc_chunks = m->doc ? w.chunks : nullptr;
   d.sh_h = bits_of(p->nH);
   d.sh_w = bits_of(p->nW);
+  d.per_plane = 1.f / ((float)p->nH * (float)p->nW);
+  d.per_row = 1.f / (float)p->nW;
   return d;
 }
 

@@ -138,9 +138,30 @@ constexpr uint32_t kSpecial = kEdge | kCausal | kDoc | kHidden;
 struct Coord {
   int t, h, w;
 };
+// a / d for 0 <= a < 2^23 with inv = 1 / d: the estimate is off by one at most.
+// A CTA's set-up is a chain of such steps; integer divisions were a third of it.
+__device__ __forceinline__ int quotient(int a, int d, float inv) {
+  const int q = (int)((float)a * inv), r = a - q * d;
+  return q + (r >= d ? 1 : 0) - (r < 0 ? 1 : 0);
+}
+// In-tile origin of a chunk (the first at once: tiles of one chunk are the usual ones).
+__device__ __forceinline__ ChunkOrigin origin_of(const Geom& g, int c) {
+  return c == 0 ? ChunkOrigin{0, 0, 0} : chunk_origin(g, c);
+}
+__device__ __forceinline__ ChunkOrigin unpack_origin(uint32_t v) {
+  return ChunkOrigin{(int)(v & 0x3FFu), (int)((v >> 10) & 0x3FFu), (int)(v >> 20)};
+}
+struct Tile {
+  int t, h, w;
+};
+__device__ __forceinline__ Tile tile_of(const Geom& g, const ModParams& m, int j) {
+  const int t = quotient(j, g.nH * g.nW, m.per_plane), rem = j - t * (g.nH * g.nW);
+  const int h = quotient(rem, g.nW, m.per_row);
+  return Tile{t, h, rem - h * g.nW};
+}
 __device__ __forceinline__ uint32_t pack_tile(const Geom& g, const ModParams& m, int j) {
-  const int bt = j / (g.nH * g.nW), rem = j - bt * (g.nH * g.nW);
-  const int bh = rem / g.nW, bw = rem - bh * g.nW;
+  const Tile x = tile_of(g, m, j);
+  const int bt = x.t, bh = x.h, bw = x.w;
   return ((uint32_t)bt << (m.sh_h + m.sh_w)) | ((uint32_t)bh << m.sh_w) | (uint32_t)bw;
 }
 // First token of the chunk at in-tile offset o of the packed tile.
@@ -155,9 +176,9 @@ struct Half {
   int lo, hi;        // frames
   int4 ids;          // (least, greatest, tokens with an id, tokens without); all 0 ids without documents
 };
-__device__ __forceinline__ Half half_of(const Geom& g, const ModParams& m, int b, int tile, int chunk) {
-  const ChunkOrigin o = chunk_origin(g, chunk);
-  const int t0 = tile / (g.nH * g.nW) * g.tt + o.dt;
+__device__ __forceinline__ Half half_of(const Geom& g, const ModParams& m, int b, int tile, int chunk,
+                                        const ChunkOrigin& o) {
+  const int t0 = quotient(tile, g.nH * g.nW, m.per_plane) * g.tt + o.dt;
   Half r{t0, min(t0 + g.ct - 1, g.T - 1), make_int4(0, 0, 1, 0)};
   if (m.doc_chunks) r.ids = __ldg(&m.doc_chunks[((size_t)b * g.N + tile) * g.nchunk + chunk].range);
   return r;
@@ -181,12 +202,14 @@ __device__ __forceinline__ bool sees(const ModParams& m, int prefix, const Half&
 // of the step list (in place, order kept) and writes each step's packed coordinates
 // and flags to ext. One side of every pair is the block's halves (queries, or
 // keys with SWAP), the other the step's chunk. All NT threads take part;
-// returns the steps left.
+// returns the steps left. origin: every chunk's packed in-tile origin (shared).
 template <int NT, bool SWAP>
 __device__ __forceinline__ int filter_steps(const Geom& g, const ModParams& m, int b, int prefix, int i0, int i1, int c0,
-                                            int c1, uint32_t* list, uint32_t* ext, int steps, int* scan) {
+                                            int c1, uint32_t* list, uint32_t* ext, int steps, int* scan,
+                                            const uint32_t* origin) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Half h0 = half_of(g, m, b, i0, c0), h1 = i1 >= 0 ? half_of(g, m, b, i1, c1) : h0;
+  const Half h0 = half_of(g, m, b, i0, c0, unpack_origin(origin[c0]));
+  const Half h1 = i1 >= 0 ? half_of(g, m, b, i1, c1, unpack_origin(origin[c1])) : h0;
   int kept = 0;
   for (int base = 0; base < steps; base += NT) {
     const int n = base + tid;
@@ -194,11 +217,11 @@ __device__ __forceinline__ int filter_steps(const Geom& g, const ModParams& m, i
     if (n < steps) {
       e = list[n];
       const int j = (int)(e & 0x1FFFFFu), c = (int)((e >> 21) & 0x1FFu);
-      const Half k = half_of(g, m, b, j, c);
+      const ChunkOrigin o = unpack_origin(origin[c]);
+      const Half k = half_of(g, m, b, j, c, o);
       if (e >> 30 & 1u && !(SWAP ? sees(m, prefix, k, h0, &x) : sees(m, prefix, h0, k, &x))) e &= ~(1u << 30);
       if (e >> 31 & 1u && !(SWAP ? sees(m, prefix, k, h1, &x) : sees(m, prefix, h1, k, &x))) e &= ~(1u << 31);
       x |= pack_tile(g, m, j);
-      const ChunkOrigin o = chunk_origin(g, c);
       const Coord f = chunk_first(g, m, x, o);
       if (g.T - f.t < g.ct || g.H - f.h < g.ch || g.W - f.w < g.cw || g.cr < 64) x |= kEdge;
       if (k.ids.w) x |= kHidden;
@@ -232,10 +255,11 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const Geom& g, const ModParams& m, int b, int tile, int chunk, uint32_t code,
                                       int r) {
-  const ChunkOrigin o = chunk_origin(g, chunk);
+  const ChunkOrigin o = origin_of(g, chunk);
+  const Tile i = tile_of(g, m, tile);
   Row x;
-  x.at = Coord{tile / (g.nH * g.nW) * g.tt + o.dt + (int)(code & 0xffu),
-               tile / g.nW % g.nH * g.th + o.dh + (int)((code >> 8) & 0xffu), tile % g.nW * g.tw + o.dw + (int)((code >> 16) & 0xffu)};
+  x.at = Coord{i.t * g.tt + o.dt + (int)(code & 0xffu), i.h * g.th + o.dh + (int)((code >> 8) & 0xffu),
+               i.w * g.tw + o.dw + (int)((code >> 16) & 0xffu)};
   x.live = r < g.cr && x.at.t < g.T && x.at.h < g.H && x.at.w < g.W;
   x.id = 0;
   if (m.doc_rows) {
@@ -255,7 +279,7 @@ struct Table {
 // Filled by all NT threads; codes of the rows in colc (shared, visible).
 template <int NT>
 __device__ __forceinline__ void fill_table(const Geom& g, Table* tab, const uint32_t* colc) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (tid < 64) {
     const uint32_t c = colc[tid];
     const float4 d = make_float4((float)(c & 0xffu), (float)((c >> 8) & 0xffu), (float)((c >> 16) & 0xffu), 0.f);
@@ -264,13 +288,15 @@ __device__ __forceinline__ void fill_table(const Geom& g, Table* tab, const uint
     tab->d[2][tid] = d.z;
     if (tid % 4 == 0) tab->group[tid / 4] = d;
   }
+  // A thread per entry: rows are ordered (t, h, w), so the first v steps of an
+  // axis are v times the inner extents' product of each of its periods.
   const int n0 = g.ct + 1, n1 = n0 + g.ch + 1, n2 = n1 + g.cw + 1;
-  const uint32_t ca = colc[lane], cb = colc[lane + 32];
-  for (int e = tid / 32; e < n2; e += NT / 32) {
+  for (int e = tid; e < n2; e += NT) {
     const int a = e < n0 ? 0 : e < n1 ? 1 : 2, v = e - (a == 0 ? 0 : a == 1 ? n0 : n1);
-    const uint32_t lo = __ballot_sync(0xffffffffu, (int)((ca >> (8 * a)) & 0xffu) < v);
-    const uint32_t hi = __ballot_sync(0xffffffffu, (int)((cb >> (8 * a)) & 0xffu) < v);
-    if (lane == 0) tab->below[a][v] = ((unsigned long long)hi << 32) | lo;
+    const int inner = a == 0 ? g.ch * g.cw : a == 1 ? g.cw : 1, period = a == 0 ? g.cr : a == 1 ? g.ch * g.cw : g.cw;
+    unsigned long long m = v * inner >= 64 ? ~0ull : (1ull << (v * inner)) - 1ull;
+    for (int p = period; p < g.cr; p *= 2) m |= m << p;
+    tab->below[a][v] = g.cr < 64 ? m & ((1ull << g.cr) - 1ull) : m;
   }
 }
 

@@ -192,16 +192,13 @@ __device__ __forceinline__ int take_share(uint32_t* list, uint32_t* ext, int ste
 struct ModTab {
   mod::Table col;
   uint32_t origin[kMaxChunks];
-  __device__ __forceinline__ ChunkOrigin at(int c) const {
-    const uint32_t v = origin[c];
-    return ChunkOrigin{(int)(v & 0x3FFu), (int)((v >> 10) & 0x3FFu), (int)(v >> 20)};
-  }
+  __device__ __forceinline__ ChunkOrigin at(int c) const { return mod::unpack_origin(origin[c]); }
 };
 template <int NT>
 __device__ __forceinline__ void fill_modtab(const Geom& g, ModTab* tab, const uint32_t* colc) {
   mod::fill_table<NT>(g, &tab->col, colc);
   for (int c = threadIdx.x; c < g.nchunk; c += NT) {
-    const ChunkOrigin o = chunk_origin(g, c);
+    const ChunkOrigin o = mod::origin_of(g, c);
     tab->origin[c] = (uint32_t)o.dt | ((uint32_t)o.dh << 10) | ((uint32_t)o.dw << 20);
   }
 }
