@@ -251,7 +251,27 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  auto load_block = [&]() {
+    tc::tma_prefetch_desc(&tmQ);
+    tc::tma_prefetch_desc(&tmDO);
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+    tc::mbar_arrive_expect_tx(bar_q, (has1 ? 2 : 1) * 2 * 64 * C::QRB);
+    for (int x = 0; x < (has1 ? 2 : 1); ++x) {
+      const int row = x ? tile_row(i1, c1) : tile_row(i0, c0);
+#pragma unroll
+      for (int cb = 0; cb < C::QBLK; ++cb) {
+        const uint32_t d = cb * 128 * 128 + x * 64 * 128;
+        tc::tma_load_2d(sb + C::OFF_Q + d, &tmQ, bar_q, cb * 64, row);
+        tc::tma_load_2d(sb + C::OFF_DO + d, &tmDO, bar_q, cb * 64, row);
+      }
+    }
+  };
   __syncthreads();
+  if (MOD) {  // while the list is made
+    if (warp == 8 && lane == 0) load_block();
+    __syncwarp();
+  }
 
   // Union of the two kept lists, ascending, one step per real 64-key chunk:
   // key tile in bits 0-20, chunk in bits 21-29, bit 30 (31) when the first
@@ -300,20 +320,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   // ------------------------------------------------------------ roles
   if (warp == 8) {
     if (lane == 0 && L > 0) {
-      tc::tma_prefetch_desc(&tmQ);
-      tc::tma_prefetch_desc(&tmDO);
-      tc::tma_prefetch_desc(&tmK);
-      tc::tma_prefetch_desc(&tmV);
-      tc::mbar_arrive_expect_tx(bar_q, (has1 ? 2 : 1) * 2 * 64 * C::QRB);
-      for (int x = 0; x < (has1 ? 2 : 1); ++x) {
-        const int row = x ? tile_row(i1, c1) : tile_row(i0, c0);
-#pragma unroll
-        for (int cb = 0; cb < C::QBLK; ++cb) {
-          const uint32_t d = cb * 128 * 128 + x * 64 * 128;
-          tc::tma_load_2d(sb + C::OFF_Q + d, &tmQ, bar_q, cb * 64, row);
-          tc::tma_load_2d(sb + C::OFF_DO + d, &tmDO, bar_q, cb * 64, row);
-        }
-      }
+      if (!MOD) load_block();
       int last[kStages];
 #pragma unroll
       for (int s = 0; s < kStages; ++s) last[s] = -1;
@@ -340,6 +347,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (last[s] >= 0) tc::mbar_wait(bar_full(s), (last[s] / kStages) & 1, never, kWaitLimit);
       }
     }
+    if (MOD && lane == 0 && L == 0) tc::mbar_wait(bar_q, 0, never, kWaitLimit);  // the block's load lands first
   } else if (warp == 9) {
     if (L > 0) {
       const uint32_t lead = tc::elect_one();
@@ -947,7 +955,27 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  auto load_block = [&]() {
+    tc::tma_prefetch_desc(&tmQ);
+    tc::tma_prefetch_desc(&tmDO);
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+    tc::mbar_arrive_expect_tx(bar_kv, (has1 ? 2 : 1) * 2 * 64 * C::QRB);
+    for (int x = 0; x < (has1 ? 2 : 1); ++x) {
+      const int row = x ? tile_row(j1, kc1) : tile_row(j0, kc0);
+#pragma unroll
+      for (int cb = 0; cb < C::QBLK; ++cb) {
+        const uint32_t d = cb * 128 * 128 + x * 64 * 128;
+        tc::tma_load_2d(sb + C::OFF_K + d, &tmK, bar_kv, cb * 64, row);
+        tc::tma_load_2d(sb + C::OFF_V + d, &tmV, bar_kv, cb * 64, row);
+      }
+    }
+  };
   __syncthreads();
+  if (MOD) {  // while the list is made
+    if (warp == 8 && lane == 0) load_block();
+    __syncwarp();
+  }
 
   // Union of the two transposed lists, ascending, one step per real chunk of
   // each listed query tile: query tile in bits 0-20, chunk in bits 21-29, bit
@@ -987,20 +1015,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // ------------------------------------------------------------ roles
   if (warp == 8) {
     if (lane == 0 && L > 0) {
-      tc::tma_prefetch_desc(&tmQ);
-      tc::tma_prefetch_desc(&tmDO);
-      tc::tma_prefetch_desc(&tmK);
-      tc::tma_prefetch_desc(&tmV);
-      tc::mbar_arrive_expect_tx(bar_kv, (has1 ? 2 : 1) * 2 * 64 * C::QRB);
-      for (int x = 0; x < (has1 ? 2 : 1); ++x) {
-        const int row = x ? tile_row(j1, kc1) : tile_row(j0, kc0);
-#pragma unroll
-        for (int cb = 0; cb < C::QBLK; ++cb) {
-          const uint32_t d = cb * 128 * 128 + x * 64 * 128;
-          tc::tma_load_2d(sb + C::OFF_K + d, &tmK, bar_kv, cb * 64, row);
-          tc::tma_load_2d(sb + C::OFF_V + d, &tmV, bar_kv, cb * 64, row);
-        }
-      }
+      if (!MOD) load_block();
       int last[kStages];
 #pragma unroll
       for (int s = 0; s < kStages; ++s) last[s] = -1;
@@ -1030,6 +1045,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (last[s] >= 0) tc::mbar_wait(bar_full(s), (last[s] / kStages) & 1, never, kWaitLimit);
       }
     }
+    if (MOD && lane == 0 && L == 0) tc::mbar_wait(bar_kv, 0, never, kWaitLimit);  // the block's load lands first
   } else if (warp == 9) {
     if (L > 0) {
       const uint32_t lead = tc::elect_one();
