@@ -23,12 +23,18 @@
 //    size, and the twelve of a step bounded the kernel (737 -> 650 us).
 //
 // Measured on one B200 (12 heads, Wan-1.3B shape, top-k 46 of 364, tiled
-// layout, 421 GFLOP on kept pairs): no rule 0.63 ms, cap 0.83, bias 0.87, both
-// 1.14; the Wan-14B shape in (6,8,8) tiles with cap and frame-causal mask 13.7
-// to 14.2 ms. Bound now by the softmax warps: a step's 64 x 128 exponentials
-// take 512 of its ~1,100 SM cycles on the SFU, the cap another 384 to 512 on
-// the FMA pipe. Eight softmax warps of 32 columns were slower (1,000 against
-// 757 us): the per-step scalar work doubles.
+// layout, 421 GFLOP on kept pairs): no rule 0.59 ms, cap 0.79, bias 0.76, both
+// 1.09; the Wan-14B shape in (6,8,8) tiles with cap and frame-causal mask 12.7
+// ms. Bound now by the softmax warps: a step's 64 x 128 exponentials take 512
+// of its ~1,050 SM cycles on the SFU, the cap another 384 to 512 on the FMA
+// pipe. Eight softmax warps of 32 columns were slower (1,000 against 757 us):
+// the per-step scalar work doubles.
+//
+// A CTA of two steps takes about 9 us of set-up, first loads and epilogue, as
+// much as nine more steps, so short lists are bound by that chain: quotients
+// by reciprocal, tables a thread per entry and Q loaded while the list is made
+// took 16K tokens in 1,024 such CTAs from 50.6 to 41.4 us, and tile windows of
+// twelve steps from 228 to 213 us.
 //
 // Roles (192 threads): warps 0-3 rules and softmax (thread r owns query row
 // r), warp 4 TMA producer, warp 5 MMA issuer. Every mbarrier wait is bounded;
@@ -826,7 +832,7 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
 // Few query blocks leave most of the GPU idle while each walks its list: up to
 // eight CTAs then share a block's steps, two per SM at most over the grid and
 // four steps each at least, and a second kernel joins their parts (two heads
-// of 8 x 16 x 16 tokens, about 20 steps a block: 46 us alone, 27 us shared).
+// of 8 x 16 x 16 tokens, about 20 steps a block: 40 us alone, 21 us shared).
 static int steps_bound(const bsattn_plan* p) {
   // The union of two lists of one-chunk tiles, or one list of tiles times their chunks.
   return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;

