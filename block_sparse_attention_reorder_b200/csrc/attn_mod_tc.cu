@@ -547,6 +547,10 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               const float alpha = raise && m != -INFINITY ? tc::ex2(m - (mx + kAbove)) : 1.f;
               if (raise) m = mx + kAbove;
               if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                // What the first half stored is read again below: its P, and O
+                // where the reference moved there too. Stores and loads of
+                // tensor memory are ordered by a wait only.
+                tc::tmem_wait_st();
                 l *= alpha;
                 if (n > 0) ok = rescale(n, alpha);
                 if (h == 1) {  // this step's first 32 probabilities

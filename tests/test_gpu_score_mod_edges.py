@@ -1,0 +1,73 @@
+"""Attention under score rules at its edges: references that move within a
+step."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rules
+from tests.helpers import to64
+from tests.test_gpu_score_mod import Case, _nan, _tiled, bs  # noqa: F401  (bs: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- references that move within a step
+
+# Score levels of the first steps of the first query block's walk, for keys 0-31 and 32-63 of a step. A row's
+# reference moves when a half's maximum is 70 powers of two (48.5) above the one that set it.
+MOVES = {  # levels of the steps, moves in the (first, second) half
+    "first": ([(-55, -55), (0, 0), (55, 55)], [(0, 0), (1, 0), (1, 0)]),
+    "second": ([(-55, -55), (-55, 0), (0, 55)], [(0, 0), (0, 1), (0, 1)]),
+    "both": ([(-55, -55), (0, 55)], [(0, 0), (1, 1)]),
+    "at_once": ([(-55, 0), (55, 0)], [(0, 1), (1, 0)]),
+}
+
+
+def _moves(z):
+    """Which halves of 32 scores (natural units, in the order of the walk) move a row's reference."""
+    ref, out = -math.inf, []
+    for half in z.reshape(-1, 32):
+        top = half.max() / math.log(2.0)
+        move = top > ref + 30.0
+        out.append(int(move and ref > -math.inf))
+        ref = top + 40.0 if move else ref
+    return [tuple(x) for x in np.array(out).reshape(-1, 2).tolist()]
+
+
+@pytest.mark.parametrize("moves", list(MOVES))
+@pytest.mark.parametrize("grid", ["seq400", "seq300_wide"])  # D = 128 and 64
+def test_references_that_move_within_a_step(bs, grid, moves):  # noqa: F811
+    """Cap and bias together take a step in two halves; what the first half stored is scaled by the second. The
+    scales are powers below 2^-70: a P or an O that missed one would outweigh all the rest."""
+    levels, want = MOVES[moves]
+    c = Case(bs, grid, "cap", seed=20)
+    plan, (T, _, _) = c.plan, c.grid
+    c.cap, c.slopes = 60.0, np.full(c.heads, 2.0 ** -10, np.float32)
+    c.mod = bs.ScoreMod(softcap=c.cap, slopes=torch.from_numpy(c.slopes).cuda(), dist=(1.0, 0.5, 0.0))
+    # The first block's walk: its own tile's chunks from the last to the first, then the others ascending.
+    per, chunks = c.tile[0] // 64, -(-T // 64)
+    walk = [*range(per)][::-1] + [*range(per, chunks)]
+    g = np.random.default_rng(23)
+    level = g.choice([-55.0, 0.0, 55.0], (chunks, 2))
+    level[walk[:len(levels)]] = levels
+    level = level.reshape(-1).repeat(32)[:T]
+    u = np.where(g.random(c.D) < 0.5, -1.0, 1.0)
+    k = (c.cap * np.arctanh(level / c.cap) / math.sqrt(c.D))[:, None] * u + 0.02 * g.standard_normal((T, c.D))
+    draw = lambda x: torch.from_numpy(np.broadcast_to(x[None, :, None], plan.natural_shape()).copy()).to(torch.bfloat16)  # noqa: E731
+    c.q, c.k = draw(u + 0.01 * g.standard_normal((T, c.D))), draw(k)
+    z = c.cap * np.tanh(c.D ** -0.5 * to64(c.q)[0, 0, 0] @ to64(c.k)[0, :, 0].T / c.cap)
+    z = z - 2.0 ** -10 * rules.distance(c.xyz[:1], c.xyz, (1.0, 0.5, 0.0))[0]
+    steps = np.concatenate([z[64 * n:64 * n + 64] for n in walk if 64 * n + 64 <= T])
+    assert _moves(steps)[:len(want)] == want
+    for ws in (None, plan.workspace("mod_forward")):
+        o, lse = _nan(plan.natural_shape()), _nan((c.B, c.heads, c.L), torch.float32)
+        bs.attn_forward_natural_mod(plan, c.mod, c.q.cuda(), c.k.cuda(), c.v.cuda(), c.idx, c.cnt, o, ws, lse_nat=lse)
+        assert bs.attn_check_device_status(plan) == 0
+        c.check_forward(to64(o), to64(lse), *(to64(x) for x in (c.q, c.k, c.v)))
+        ot = _nan(plan.tiled_shape())
+        bs.attn_forward_mod(plan, c.mod, *_tiled(bs, plan, c.q, c.k, c.v), c.idx, c.cnt, ot, ws)
+        back = torch.empty_like(o)
+        bs.attn_unreorder(plan, ot, back)
+        assert torch.equal(back, o)
