@@ -677,7 +677,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
       }
     } else {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a sum that is no number stays one, as where parts are joined
       uint8_t* stage = smem + C::OFF_K + r * C::O_PITCH;
 #pragma unroll
       for (int col = 0; col < D; col += 32) {
@@ -698,7 +698,7 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       if (P.lse && row_exists) {
         // In terms of the maximum, so that no rounding of m's size enters.
-        const float lse_r = l > 0.f ? ((m - kAbove) + log2f(l * kAboveUnit)) * 0.69314718055994531f : -INFINITY;
+        const float lse_r = l == 0.f ? -INFINITY : ((m - kAbove) + log2f(l * kAboveUnit)) * 0.69314718055994531f;
         if (NAT) {
           if (tokrow[r] >= 0) P.lse[bh * (size_t)g.L + (size_t)tokrow[r]] = lse_r;
         } else {

@@ -1,5 +1,5 @@
 """Attention under score rules at its edges: references that move within a
-step."""
+step, and rows that are not numbers."""
 import math
 
 import numpy as np
@@ -71,3 +71,41 @@ def test_references_that_move_within_a_step(bs, grid, moves):  # noqa: F811
         back = torch.empty_like(o)
         bs.attn_unreorder(plan, ot, back)
         assert torch.equal(back, o)
+
+
+# ---------------------------------------------------------------- rows that are not numbers
+
+@pytest.mark.parametrize("rule", ["cap", "bias", "all"])
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("grid", ["ragged", "seq400"])
+def test_a_visible_row_that_is_not_a_number(bs, grid, shared, rule):  # noqa: F811
+    """NaN in a visible query row: O, lse and dQ of that row are NaN, whether CTAs share its block or not; its
+    lse is not the -inf of a row that sees no key. Other rows of O and dQ are what they are without it."""
+    c = Case(bs, grid, rule, seed=21)
+    plan, ws = c.plan, c.plan.workspace("mod_forward") if shared or c.doc is not None else None
+    # The first token of the last batch that sees a key.
+    b, h = c.B - 1, c.heads - 1
+    r = c.oracle(b, h, *(to64(x)[b, :, h] for x in (c.q, c.k, c.v)))
+    row = int((~(r["lse"] == -float("inf"))).nonzero()[0][0])
+    bad = c.q.clone()
+    bad[b, row, h, 5] = float("nan")
+    res = []
+    for q0 in (c.q, bad):
+        o, lse = _nan(plan.natural_shape()), _nan((c.B, c.heads, c.L), torch.float32)
+        bs.attn_forward_natural_mod(plan, c.mod, q0.cuda(), c.k.cuda(), c.v.cuda(), c.idx, c.cnt, o, ws, lse_nat=lse)
+        q, k, v, do = _tiled(bs, plan, q0, c.k, c.v, c.do)
+        ot, lt = _nan(plan.tiled_shape()), _nan(plan.tiled_shape()[:-1], torch.float32)
+        bs.attn_forward_mod(plan, c.mod, q, k, v, c.idx, c.cnt, ot, ws, lse=lt)
+        grads = [_nan(plan.tiled_shape()) for _ in range(3)]
+        bs.attn_backward_mod(plan, c.mod, q, k, v, ot, do, lt, c.idx, c.cnt, *grads, plan.workspace("mod_backward"))
+        assert bs.attn_check_device_status(plan) == 0
+        dq = torch.empty_like(o)
+        bs.attn_unreorder(plan, grads[0], dq)
+        res.append((o, dq, lse))
+    (o0, dq0, lse0), (o1, dq1, lse1) = res
+    assert torch.isnan(o1[b, row, h]).all() and torch.isnan(dq1[b, row, h]).all() and torch.isnan(lse1[b, h, row])
+    for x, y in ((o0, o1), (dq0, dq1)):
+        y[b, row, h] = x[b, row, h]
+        assert torch.equal(x, y)
+    lse1[b, h, row] = lse0[b, h, row]
+    assert torch.equal(lse0, lse1)
