@@ -244,13 +244,21 @@ static inline int attention_items(const bsattn_plan* p) {
   return p->N / nd[a] * ((nd[a] + 1) / 2);
 }
 
-bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r);
-// Rotation of one or two natural tensors (r null: a copy), with fp32 tile means
+// A checked rotation: pairs ordered t, h, w with their frequencies.
+struct RopeTurns {
+  int npairs;                    // R
+  int split[2];                  // first pair of the h and w axes
+  unsigned long long turns[64];  // f / (2 pi) modulo 1, in 2^-64
+};
+// Checks the description and forms its frequencies, so that nothing is left to
+// refuse once work is enqueued.
+bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r, RopeTurns* out);
+// Rotation of one or two natural tensors (r null: a copy; turns: check_rope's), with fp32 tile means
 // where asked. doc, if given ([B, L]): tokens with a negative id are written as
 // zeros and left out of the means (0 for a tile of such tokens only).
-bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv_bfloat16* x0, __nv_bfloat16* y0,
-                          const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1, bool transpose,
-                          const int32_t* doc, cudaStream_t st);
+bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const RopeTurns& turns, const __nv_bfloat16* x0,
+                          __nv_bfloat16* y0, const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1,
+                          bool transpose, const int32_t* doc, cudaStream_t st);
 
 // Natural-layout tensor map [B, T, H, W, heads * D] whose box is one chunk.
 bool bsattn_make_map_nat(CUtensorMap* map, const void* base, const bsattn_plan* p);

@@ -41,14 +41,12 @@ struct RopeParams {
   const int32_t* pos;   // [B, L, 3] or null
   const int32_t* doc;   // [B, L] or null: tokens with a negative id become zeros and count in no mean
   int off[3];
-  int npairs;           // R
-  int split[2];         // first pair of the h and w axes
+  RopeTurns turn;
   float amp;
   float sign;           // -1: transposed rotation
   int hblk;             // head blocks per tensor
   int by_tile;          // a CTA takes a whole tile (tile means)
   int nu, rg;           // units per head, rows taken at once
-  unsigned long long turns[64];  // f / (2 pi) modulo 1, in 2^-64
 };
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -84,7 +82,7 @@ rope_kernel(const __grid_constant__ RopeParams P) {
   __shared__ int seen;                // tokens in the sums
   __shared__ float part[POOL ? kThreads * kHeads * NV : 1];
   const Geom& g = P.g;
-  const int D = g.D, R = P.npairs, tid = threadIdx.x;
+  const int D = g.D, R = P.turn.npairs, tid = threadIdx.x;
   // Head blocks vary fastest, so that CTAs that run together read whole token
   // rows (all heads of a token are contiguous).
   const int tensor = blockIdx.z, b = blockIdx.y, head0 = blockIdx.x % P.hblk * kHeads, item = blockIdx.x / P.hblk;
@@ -115,7 +113,7 @@ rope_kernel(const __grid_constant__ RopeParams P) {
   // Shift that takes a pair's axis out of rowval.
   uint32_t shift[NP];
 #pragma unroll
-  for (int e = 0; e < NP; ++e) shift[e] = p0 + e < P.split[0] ? 0 : p0 + e < P.split[1] ? 8 : 16;
+  for (int e = 0; e < NP; ++e) shift[e] = p0 + e < P.turn.split[0] ? 0 : p0 + e < P.turn.split[1] ? 8 : 16;
   const size_t row_el = (size_t)g.Hh * D;
   const size_t base = (size_t)b * g.L * row_el + (size_t)head0 * D;
   const int nh = min(kHeads, g.Hh - head0);
@@ -158,9 +156,9 @@ rope_kernel(const __grid_constant__ RopeParams P) {
     // The table: thread tid takes pair tid % 64 of every second value.
     const int p = tid % 64;
     if (p < R) {
-      const int a = p < P.split[0] ? 0 : p < P.split[1] ? 1 : 2;
+      const int a = p < P.turn.split[0] ? 0 : p < P.turn.split[1] ? 1 : 2;
       const int vals = P.pos ? g.cr : a == 0 ? g.ct : a == 1 ? g.ch : g.cw;
-      const unsigned long long f = P.turns[p];
+      const unsigned long long f = P.turn.turns[p];
       const long long at0 = (long long)P.off[a] + (a == 0 ? t0 : a == 1 ? h0 : w0);
       for (int v = tid / 64; v < vals; v += kThreads / 64) {
         const long long at = P.pos ? rowpos[a][v] : at0 + v;
@@ -309,14 +307,14 @@ rope_kernel(const __grid_constant__ RopeParams P) {
 template <int MODE>
 bsattn_status run(RopeParams& prm, int ntensor, bool pool, cudaStream_t st) {
   const Geom& g = prm.g;
-  prm.nu = MODE == kInterleaved ? g.D / 8 : MODE == kHalf8 ? (g.D - prm.npairs) / 8 : g.D / 2;
+  prm.nu = MODE == kInterleaved ? g.D / 8 : MODE == kHalf8 ? (g.D - prm.turn.npairs) / 8 : g.D / 2;
   prm.rg = kThreads / prm.nu;  // nu <= 64
   prm.hblk = (g.Hh + kHeads - 1) / kHeads;
   prm.by_tile = pool ? 1 : 0;
   const long long gx = (pool ? g.N : (long long)g.N * g.nchunk) * prm.hblk;
   if (g.B > 65535 || gx > 0x7fffffffLL) return BSATTN_ERR_UNSUPPORTED;
   const int box = g.ct > g.ch ? (g.ct > g.cw ? g.ct : g.cw) : (g.ch > g.cw ? g.ch : g.cw);
-  const size_t smem = (size_t)(prm.pos ? g.cr : box) * prm.npairs * sizeof(float2);  // <= 32 KB
+  const size_t smem = (size_t)(prm.pos ? g.cr : box) * prm.turn.npairs * sizeof(float2);  // <= 32 KB
   if (pool && smem > 14 * 1024) {  // with the exchange buffer (33 KB at most) above the default 48 KB
     if (cudaFuncSetAttribute(rope_kernel<MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024) != cudaSuccess)
       return BSATTN_ERR_CUDA;
@@ -331,7 +329,16 @@ bsattn_status run(RopeParams& prm, int ntensor, bool pool, cudaStream_t st) {
 
 }  // namespace
 
-bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r) {
+// x modulo 1 (x >= 0), in units of 2^-64.
+static unsigned long long fraction64(double x) {
+  x -= floor(x);
+  const double hi = floor(x * 0x1p32);
+  const double lo = floor((x * 0x1p32 - hi) * 0x1p32);
+  return ((unsigned long long)hi << 32) | (unsigned long long)lo;
+}
+
+bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r, RopeTurns* out) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
   if (r->layout != BSATTN_ROPE_INTERLEAVED && r->layout != BSATTN_ROPE_HALF) return BSATTN_ERR_INVALID_ARG;
   if (r->scaling < BSATTN_ROPE_SCALE_NONE || r->scaling > BSATTN_ROPE_SCALE_BY_PARTS) return BSATTN_ERR_INVALID_ARG;
   long long sum = 0;
@@ -350,53 +357,46 @@ bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r) {
     if (!(r->slow >= 0.0) || !(r->fast > r->slow) || !isfinite(r->fast)) return BSATTN_ERR_INVALID_ARG;
   }
   if (r->pos && !aligned16(r->pos)) return BSATTN_ERR_INVALID_ARG;
+  int np = 0;
+  for (int a = 0; a < 3; ++a) {
+    const int d = r->dim[a];
+    if (a > 0) out->split[a - 1] = np;
+    const double s = r->factor[a];
+    double base = r->base;
+    if (r->scaling == BSATTN_ROPE_SCALE_NTK && d > 2) base *= pow(s, (double)d / (d - 2));
+    // exp2 of the rounded exponent: within 1e-7 of a radian at position 2^31.
+    const double per_pair = d > 0 ? -2.0 * log2(base) / d : 0.0;
+    for (int i = 0; i < d / 2; ++i) {
+      double f = exp2(per_pair * i);
+      if (r->scaling == BSATTN_ROPE_SCALE_LINEAR) f /= s;
+      if (r->scaling == BSATTN_ROPE_SCALE_BY_PARTS) {
+        double keep = (r->original[a] * f / kTwoPi - r->slow) / (r->fast - r->slow);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        f *= keep + (1.0 - keep) / s;
+      }
+      const double turn = f / kTwoPi;
+      if (!isfinite(turn)) return BSATTN_ERR_INVALID_ARG;  // extreme factors
+      out->turns[np++] = fraction64(turn);
+    }
+  }
+  out->npairs = np;
   return BSATTN_OK;
 }
 
-// x modulo 1 (x >= 0), in units of 2^-64.
-static unsigned long long fraction64(double x) {
-  x -= floor(x);
-  const double hi = floor(x * 0x1p32);
-  const double lo = floor((x * 0x1p32 - hi) * 0x1p32);
-  return ((unsigned long long)hi << 32) | (unsigned long long)lo;
-}
-
-bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const __nv_bfloat16* x0, __nv_bfloat16* y0,
-                          const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1, bool transpose,
-                          const int32_t* doc, cudaStream_t st) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
+bsattn_status launch_rope(const bsattn_plan* p, const bsattn_rope* r, const RopeTurns& turns, const __nv_bfloat16* x0,
+                          __nv_bfloat16* y0, const __nv_bfloat16* x1, __nv_bfloat16* y1, float* pooled0, float* pooled1,
+                          bool transpose, const int32_t* doc, cudaStream_t st) {
   RopeParams prm{};
   prm.g = make_geom(p);
   prm.doc = doc;
-  int np = 0;
   if (r) {
     prm.pos = r->pos;
     prm.amp = r->amplitude == 0.0 ? 1.f : (float)r->amplitude;
     prm.sign = transpose ? -1.f : 1.f;
-    for (int a = 0; a < 3; ++a) {
-      prm.off[a] = r->offset[a];
-      const int d = r->dim[a];
-      if (a > 0) prm.split[a - 1] = np;
-      const double s = r->factor[a];
-      double base = r->base;
-      if (r->scaling == BSATTN_ROPE_SCALE_NTK && d > 2) base *= pow(s, (double)d / (d - 2));
-      // exp2 of the rounded exponent: within 1e-7 of a radian at position 2^31.
-      const double per_pair = d > 0 ? -2.0 * log2(base) / d : 0.0;
-      for (int i = 0; i < d / 2; ++i) {
-        double f = exp2(per_pair * i);
-        if (r->scaling == BSATTN_ROPE_SCALE_LINEAR) f /= s;
-        if (r->scaling == BSATTN_ROPE_SCALE_BY_PARTS) {
-          double keep = (r->original[a] * f / kTwoPi - r->slow) / (r->fast - r->slow);
-          keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-          f *= keep + (1.0 - keep) / s;
-        }
-        const double turn = f / kTwoPi;
-        if (!isfinite(turn)) return BSATTN_ERR_INVALID_ARG;  // extreme factors
-        prm.turns[np++] = fraction64(turn);
-      }
-    }
+    for (int a = 0; a < 3; ++a) prm.off[a] = r->offset[a];
+    prm.turn = turns;
   }
-  prm.npairs = np;
+  const int np = prm.turn.npairs;
   const bool interleaved = !r || r->layout == BSATTN_ROPE_INTERLEAVED;
   // One launch when both tensors want the same outputs (the usual call), else one each.
   const bool one = x1 && (pooled0 != nullptr) == (pooled1 != nullptr);
@@ -420,10 +420,11 @@ extern "C" bsattn_status attn_rope(const bsattn_plan* p, const bsattn_rope* r, c
     return BSATTN_ERR_INVALID_ARG;
   if ((pooled0 && !aligned16(pooled0)) || (pooled1 && (!aligned16(pooled1) || !x1))) return BSATTN_ERR_INVALID_ARG;
   if (transpose != 0 && transpose != 1) return BSATTN_ERR_INVALID_ARG;
-  bsattn_status s = check_rope(p, r);
+  RopeTurns turns{};
+  bsattn_status s = check_rope(p, r, &turns);
   if (s) return s;
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
-  return launch_rope(p, r, (const __nv_bfloat16*)x0, (__nv_bfloat16*)y0, (const __nv_bfloat16*)x1, (__nv_bfloat16*)y1,
+  return launch_rope(p, r, turns, (const __nv_bfloat16*)x0, (__nv_bfloat16*)y0, (const __nv_bfloat16*)x1, (__nv_bfloat16*)y1,
                      pooled0, pooled1, transpose != 0, nullptr, (cudaStream_t)stream);
 }

@@ -458,7 +458,8 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
       !aligned16(idx_out) || !aligned16(cnt_out) || ((idx_out == nullptr) != (cnt_out == nullptr)))
     return BSATTN_ERR_INVALID_ARG;
   bsattn_status s = BSATTN_OK;
-  if (rope && (s = check_rope(p, rope))) return s;
+  RopeTurns turns{};
+  if (rope && (s = check_rope(p, rope, &turns))) return s;
   if (m && (s = check_mod(m))) return s;
   Carve size(nullptr);
   carve_layer_mod(p, size);
@@ -478,7 +479,7 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
   // Rotated copies with their tile means; documents need them too where tile
   // means or tile scales are taken, because hidden tokens must not enter those.
   if (rope || (doc && (route || p->desc.qk_fp8))) {
-    if ((s = launch_rope(p, rope, (const __nv_bfloat16*)q_nat, w.q, (const __nv_bfloat16*)k_nat, w.k,
+    if ((s = launch_rope(p, rope, turns, (const __nv_bfloat16*)q_nat, w.q, (const __nv_bfloat16*)k_nat, w.k,
                          route ? w.pq : nullptr, route ? w.pk : nullptr, false, doc, st)))
       return s;
     q = w.q;

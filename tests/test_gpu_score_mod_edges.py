@@ -1,5 +1,5 @@
 """Attention under score rules at its edges: references that move within a
-step, and rows that are not numbers."""
+step, rows that are not numbers, and refusals, which come before any work."""
 import math
 
 import numpy as np
@@ -109,3 +109,25 @@ def test_a_visible_row_that_is_not_a_number(bs, grid, shared, rule):  # noqa: F8
         assert torch.equal(x, y)
     lse1[b, h, row] = lse0[b, h, row]
     assert torch.equal(lse0, lse1)
+
+
+# ---------------------------------------------------------------- refusals come before any work
+
+def _marked(nbytes):
+    return torch.full((int(nbytes),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def _docs(plan):
+    return torch.zeros((plan.B, plan.L), dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("rule", ["topk", "window"])
+def test_refused_frequencies_leave_everything_as_it_was(bs, rule):  # noqa: F811
+    plan = bs.Plan(1, 2, 128, 4, 8, 8, rule=rule, k=2, win=(1, 1, 1))
+    x = torch.zeros(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")
+    o, ws = _nan(plan.natural_shape()), _marked(plan.mod_info.layer_workspace_bytes)
+    r = bs.Rope(dims=(8, 8, 8), scaling="ntk", factor=(1.0, 1e300, 1.0))
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_layer_mod(plan, r, bs.ScoreMod(softcap=5.0, doc=_docs(plan)), x, x, x, o, ws)
+    assert e.value.code == 1
+    assert torch.isnan(o).all() and torch.all(ws == 0xA5)
