@@ -792,12 +792,19 @@ __global__ void __launch_bounds__(kJoinRows * D / 8) attn_join_kernel(const __gr
     P.lse[NAT ? bh * (size_t)g.L + out : out] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
+// Fixed part, two list bitmaps, step list, coordinates and (e4m3) scales.
+template <int D, bool FP8>
+size_t smem_bytes(const bsattn_plan* p) {
+  const size_t smem = 1024 + Cfg<D, FP8>::OFF_DYN + (size_t)((p->N + 31) / 32) * 8 +
+                      (size_t)attention_steps(p) * (FP8 ? 12 : 8);
+  return smem < 80 * 1024 ? 80 * 1024 : smem;  // at most two CTAs (2 x 256 TMEM columns) per SM
+}
+
 template <int D, bool FP8, bool NAT, bool CAP, bool BIAS>
 bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v, const Params& prm,
                   cudaStream_t st) {
   using C = Cfg<D, FP8>;
-  const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
-  if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  const uint64_t rows = tiled_rows(p);
   CUtensorMap mq, mk, mv;
   const CUtensorMapDataType dqk = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = C::SWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -808,9 +815,7 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
   if (NAT ? !bsattn_make_map_nat(&mv, v, p)
           : !bsattn_make_map_2d(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return BSATTN_ERR_CUDA;
-  size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * (FP8 ? 12 : 8);
-  if (smem < 80 * 1024) smem = 80 * 1024;  // at most two CTAs (2 x 256 TMEM columns) per SM
-  if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
+  const size_t smem = smem_bytes<D, FP8>(p);
   auto kern = attn_mod_tc_kernel<D, FP8, NAT, CAP, BIAS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
@@ -837,14 +842,10 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
 // eight CTAs then share a block's steps, two per SM at most over the grid and
 // four steps each at least, and a second kernel joins their parts (two heads
 // of 8 x 16 x 16 tokens, about 20 steps a block: 40 us alone, 21 us shared).
-static int steps_bound(const bsattn_plan* p) {
-  // The union of two lists of one-chunk tiles, or one list of tiles times their chunks.
-  return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
-}
 static int attention_parts(const bsattn_plan* p) {
   const long long blocks = (long long)attention_items(p) * p->desc.heads * p->desc.B;
   long long parts = 2 * 148 / blocks;
-  if (parts > steps_bound(p) / 4) parts = steps_bound(p) / 4;
+  if (parts > attention_steps(p) / 4) parts = attention_steps(p) / 4;
   return parts < 2 ? 1 : parts > kMaxParts ? kMaxParts : (int)parts;
 }
 size_t attention_mod_workspace_bytes(const bsattn_plan* p) {
@@ -854,11 +855,19 @@ size_t attention_mod_workspace_bytes(const bsattn_plan* p) {
   return rows * ((size_t)p->desc.head_dim * sizeof(float) + sizeof(float2));
 }
 
+bsattn_status check_attention_mod(const bsattn_plan* p) {
+  if (p->N > 32768 || tiled_rows(p) + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  if (p->desc.B > 65535 || p->desc.heads > 65535) return BSATTN_ERR_UNSUPPORTED;  // grid
+  const bool fp8 = p->desc.qk_fp8 != 0, d128 = p->desc.head_dim == 128;
+  const size_t smem = d128 ? (fp8 ? smem_bytes<128, true>(p) : smem_bytes<128, false>(p))
+                           : (fp8 ? smem_bytes<64, true>(p) : smem_bytes<64, false>(p));
+  return smem > 227 * 1024 ? BSATTN_ERR_UNSUPPORTED : BSATTN_OK;
+}
+
 bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
                                    const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
                                    const int32_t* cnt, __nv_bfloat16* o, float* lse, void* ws, cudaStream_t st,
                                    AttnLayout lay) {
-  if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
   Params prm;
   prm.g = make_geom(p);
   prm.mod = mod;
@@ -871,7 +880,7 @@ bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, c
   prm.lse = lse;
   prm.scale = p->scale;
   prm.err = p->d_err;
-  prm.umax = steps_bound(p);
+  prm.umax = attention_steps(p);
   prm.parts = ws ? attention_parts(p) : 1;
   prm.part_o = (float*)ws;
   prm.part_ml = nullptr;

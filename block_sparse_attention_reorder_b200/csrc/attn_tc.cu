@@ -753,12 +753,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host side
+// Fixed part, two list bitmaps, step list, extents, (tiles of several chunks)
+// chunk offsets and (e4m3) scales.
+template <int D, bool FP8>
+size_t smem_bytes(const bsattn_plan* p) {
+  const size_t smem = 1024 + Cfg<D, FP8>::OFF_DYN + (size_t)((p->N + 31) / 32) * 8 +
+                      (size_t)attention_steps(p) * ((p->nchunk > 1 ? 12 : 8) + (FP8 ? 4 : 0));
+  return smem < 80 * 1024 ? 80 * 1024 : smem;  // at most two CTAs (2 x 256 TMEM columns) per SM
+}
+
 template <int D, bool FP8, bool NAT>
 bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv_bfloat16* v,
                   TcParams prm, cudaStream_t st) {
   using C = Cfg<D, FP8>;
-  const uint64_t rows = (uint64_t)p->desc.B * p->desc.heads * p->N * p->V;
-  if (rows + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  const uint64_t rows = tiled_rows(p);
   CUtensorMap mq, mk, mv;
   const CUtensorMapDataType dqk = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = C::SWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -769,11 +777,7 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
   if (NAT ? !bsattn_make_map_nat(&mv, v, p)
           : !bsattn_make_map_2d(&mv, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return BSATTN_ERR_CUDA;
-  // Step list, extents and (tiles of several chunks) chunk offsets.
-  size_t smem = 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * (p->nchunk > 1 ? 12 : 8) +
-                (FP8 ? (size_t)prm.umax * 4 : 0);
-  if (smem < 80 * 1024) smem = 80 * 1024;  // at most two CTAs (2 x 256 TMEM columns) per SM
-  if (smem > 227 * 1024) return BSATTN_ERR_UNSUPPORTED;
+  const size_t smem = smem_bytes<D, FP8>(p);
   auto kern = attn_tc_kernel<D, FP8, NAT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return BSATTN_ERR_CUDA;
@@ -787,11 +791,20 @@ bsattn_status run(const bsattn_plan* p, const void* q, const void* k, const __nv
 
 size_t attention_workspace_bytes(const bsattn_plan*) { return 0; }
 
+bsattn_status check_attention(const bsattn_plan* p) {
+  if (p->N > 32768 || tiled_rows(p) + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  const bool fp8 = p->desc.qk_fp8 != 0, d128 = p->desc.head_dim == 128;
+  const size_t smem = d128 ? (fp8 ? smem_bytes<128, true>(p) : smem_bytes<128, false>(p))
+                           : (fp8 ? smem_bytes<64, true>(p) : smem_bytes<64, false>(p));
+  return smem > 227 * 1024 ? BSATTN_ERR_UNSUPPORTED : BSATTN_OK;
+}
+
 bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* k, const float* qs,
                                const float* ks, const __nv_bfloat16* v, const int32_t* idx,
                                const int32_t* cnt, __nv_bfloat16* o, float* lse, void*, size_t,
                                cudaStream_t st, AttnLayout lay) {
-  if (p->N > 32768) return BSATTN_ERR_UNSUPPORTED;
+  const bsattn_status s = check_attention(p);
+  if (s) return s;
   TcParams prm;
   prm.g = make_geom(p);
   prm.qs = qs;
@@ -803,10 +816,7 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
   prm.lse = lse;
   prm.scale_log2 = p->scale * 1.4426950408889634f;
   prm.err = p->d_err;
-  // Step-list capacity: the union of two lists of one-chunk tiles, or one
-  // list of tiles times their chunks.
-  prm.umax = p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax)
-                            : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+  prm.umax = attention_steps(p);
   prm.bm_words = (p->N + 31) / 32;
   prm.pair_axis = pair_axis_of(p);
   prm.stall = bsattn_testing_timeout_forced() ? 1 : 0;

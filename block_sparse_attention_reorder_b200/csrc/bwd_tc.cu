@@ -1421,25 +1421,17 @@ bsattn_status run_dkdv(const bsattn_plan* p, const void* q, const void* k, const
 
 }  // namespace
 
-// Shared memory of a launch: the configuration's fixed part, two list bitmaps
-// and two words per step.
-template <class C, class P>
-static size_t smem_of(const P& prm) {
-  return 1024 + C::OFF_DYN + (size_t)prm.bm_words * 8 + (size_t)prm.umax * 8;
-}
-// Whether a fourth ring stage leaves room for the step lists. Under score
-// rules a stage is released by the S product two steps on, which leaves three
-// stages one step for a load's latency and four stages two.
-template <class C, class P>
-static bool fits(const P& prm) {
-  return smem_of<C>(prm) <= 227 * 1024;
+// Whether the step lists fit: shared memory of a launch is the configuration's
+// fixed part, two list bitmaps and two words per step. Under score rules a
+// stage is released by the S product two steps on, which leaves three ring
+// stages one step for a load's latency and four stages two, so four are taken
+// where they fit.
+template <class C>
+static bool fits(const bsattn_plan* p, int steps) {
+  return 1024 + C::OFF_DYN + (size_t)((p->N + 31) / 32) * 8 + (size_t)steps * 8 <= 227 * 1024;
 }
 
-// Most steps a block may have: the union of two kept lists (one list for tiles
-// of several chunks) or, for key blocks, all query tiles, times the chunks.
-static int query_steps(const bsattn_plan* p) {
-  return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
-}
+// Most steps of a key block: all query tiles times their chunks.
 static int key_steps(const bsattn_plan* p) { return p->N * p->nchunk; }
 // Under score rules, on grids that leave half of the SMs or more idle, up to
 // eight CTAs share a block's steps, one per SM over the grid and four steps
@@ -1459,13 +1451,22 @@ static size_t share_rows(const bsattn_plan* p, int shares) {
   return shares == 1 ? 0 : (size_t)attention_items(p) * p->desc.heads * p->desc.B * shares * 128;
 }
 size_t backward_mod_workspace_bytes(const bsattn_plan* p) {
-  const size_t d = p->desc.head_dim, nq = share_rows(p, backward_shares(p, query_steps(p))),
+  const size_t d = p->desc.head_dim, nq = share_rows(p, backward_shares(p, attention_steps(p))),
                nk = share_rows(p, backward_shares(p, key_steps(p)));
   const size_t a = nq * (2 * d * sizeof(float) + sizeof(float4)), b = nk * 2 * d * sizeof(float);
   return a > b ? a : b;  // the passes follow one another
 }
 int backward_slope_items(const bsattn_plan* p) {
-  return attention_items(p) * (backward_shares(p, query_steps(p)) > 1 ? kJoinBlocks : 1);
+  return attention_items(p) * (backward_shares(p, attention_steps(p)) > 1 ? kJoinBlocks : 1);
+}
+
+bsattn_status check_backward_mod(const bsattn_plan* p) {
+  if (tiled_rows(p) + 128 >= (1ull << 31)) return BSATTN_ERR_UNSUPPORTED;
+  if (p->desc.B > 65535 || p->desc.heads > 65535) return BSATTN_ERR_UNSUPPORTED;  // grid
+  const int q = attention_steps(p), k = key_steps(p);
+  const bool ok = p->desc.head_dim == 128 ? fits<DqCfg<128, true, 3>>(p, q) && fits<KvCfg<128, true, 3>>(p, k)
+                                          : fits<DqCfg<64, true, 3>>(p, q) && fits<KvCfg<64, true, 3>>(p, k);
+  return ok ? BSATTN_OK : BSATTN_ERR_UNSUPPORTED;
 }
 
 bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const void* k, const void* v,
@@ -1483,7 +1484,7 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
   prm.scale = p->scale;
   prm.scale_log2 = p->scale * 1.4426950408889634f;
   prm.err = p->d_err;
-  prm.umax = query_steps(p);
+  prm.umax = attention_steps(p);
   prm.bm_words = (p->N + 31) / 32;
   prm.pair_axis = pair_axis_of(p);
   const int nd[3] = {p->nT, p->nH, p->nW};
@@ -1498,10 +1499,10 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
     prm.part_q = (float*)shares;
     prm.part_s = (float4*)(prm.part_q + share_rows(p, prm.shares) * 2 * p->desc.head_dim);
     if (d128)
-      return fits<DqCfg<128, true, 4>>(prm) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)
-                                            : run_dq<128, true, 3>(p, q, k, v, d_o, prm, st);
-    return fits<DqCfg<64, true, 4>>(prm) ? run_dq<64, true, 4>(p, q, k, v, d_o, prm, st)
-                                         : run_dq<64, true, 3>(p, q, k, v, d_o, prm, st);
+      return fits<DqCfg<128, true, 4>>(p, prm.umax) ? run_dq<128, true, 4>(p, q, k, v, d_o, prm, st)
+                                                    : run_dq<128, true, 3>(p, q, k, v, d_o, prm, st);
+    return fits<DqCfg<64, true, 4>>(p, prm.umax) ? run_dq<64, true, 4>(p, q, k, v, d_o, prm, st)
+                                                 : run_dq<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
   return d128 ? run_dq<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dq<64, false, 3>(p, q, k, v, d_o, prm, st);
 }
@@ -1532,10 +1533,10 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
     prm.shares = backward_shares(p, prm.umax);
     prm.part_kv = (float*)shares;
     if (d128)
-      return fits<KvCfg<128, true, 4>>(prm) ? run_dkdv<128, true, 4>(p, q, k, v, d_o, prm, st)
-                                            : run_dkdv<128, true, 3>(p, q, k, v, d_o, prm, st);
-    return fits<KvCfg<64, true, 4>>(prm) ? run_dkdv<64, true, 4>(p, q, k, v, d_o, prm, st)
-                                         : run_dkdv<64, true, 3>(p, q, k, v, d_o, prm, st);
+      return fits<KvCfg<128, true, 4>>(p, prm.umax) ? run_dkdv<128, true, 4>(p, q, k, v, d_o, prm, st)
+                                                    : run_dkdv<128, true, 3>(p, q, k, v, d_o, prm, st);
+    return fits<KvCfg<64, true, 4>>(p, prm.umax) ? run_dkdv<64, true, 4>(p, q, k, v, d_o, prm, st)
+                                                 : run_dkdv<64, true, 3>(p, q, k, v, d_o, prm, st);
   }
   return d128 ? run_dkdv<128, false, 3>(p, q, k, v, d_o, prm, st) : run_dkdv<64, false, 3>(p, q, k, v, d_o, prm, st);
 }

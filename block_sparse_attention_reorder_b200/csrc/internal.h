@@ -185,8 +185,12 @@ bsattn_status launch_attention(const bsattn_plan* p, const void* q, const void* 
                                const int32_t* idx, const int32_t* cnt, __nv_bfloat16* o,
                                float* lse, void* ws, size_t ws_bytes, cudaStream_t st,
                                AttnLayout lay);
-// The same under score rules (csrc/attn_mod_tc.cu). ws: scratch of
-// attention_mod_workspace_bytes, or null (then no CTAs share a query block).
+// What launch_attention refuses, to be asked before a call enqueues anything.
+bsattn_status check_attention(const bsattn_plan* p);
+// The same under score rules (csrc/attn_mod_tc.cu), for plans that
+// check_attention_mod accepts. ws: scratch of attention_mod_workspace_bytes, or
+// null (then no CTAs share a query block).
+bsattn_status check_attention_mod(const bsattn_plan* p);
 size_t attention_mod_workspace_bytes(const bsattn_plan* p);
 bsattn_status launch_attention_mod(const bsattn_plan* p, const ModParams& mod, const void* q, const void* k,
                                    const float* qs, const float* ks, const __nv_bfloat16* v, const int32_t* idx,
@@ -227,8 +231,9 @@ bsattn_status launch_backward_dq_tc(const bsattn_plan* p, const void* q, const v
                                     const void* d_o, const float* lse, float* delta, const int32_t* idx,
                                     const int32_t* cnt, void* dq, cudaStream_t st, const ModParams* mod = nullptr,
                                     float* neg_lse2 = nullptr, float* slope_parts = nullptr, void* shares = nullptr);
-// With score rules: scratch of both passes (`shares`), and the slope gradient's
-// parts per (batch, head).
+// With score rules: what either pass refuses, to be asked before the first is
+// enqueued; scratch of both (`shares`); and the slope gradient's parts per (batch, head).
+bsattn_status check_backward_mod(const bsattn_plan* p);
 size_t backward_mod_workspace_bytes(const bsattn_plan* p);
 int backward_slope_items(const bsattn_plan* p);
 
@@ -237,6 +242,13 @@ bsattn_status launch_backward_dkdv_tc(const bsattn_plan* p, const void* q, const
                                       const void* d_o, const float* lse, const float* delta, const int32_t* idxT,
                                       const int32_t* cntT, void* dk, void* dv, cudaStream_t st,
                                       const ModParams* mod = nullptr, void* shares = nullptr);
+// Rows of a tiled tensor.
+static inline uint64_t tiled_rows(const bsattn_plan* p) { return (uint64_t)p->desc.B * p->desc.heads * p->N * p->V; }
+// Most steps of a query block: the union of two lists of one-chunk tiles, or
+// one list of tiles times their chunks.
+static inline int attention_steps(const bsattn_plan* p) {
+  return p->nchunk == 1 ? (p->N < 2 * p->kmax ? p->N : 2 * p->kmax) : (p->N < p->kmax ? p->N : p->kmax) * p->nchunk;
+}
 // CTAs of the attention kernels per (batch, head): 128-row query (key) blocks.
 static inline int attention_items(const bsattn_plan* p) {
   if (p->nchunk > 1) return p->N * ((p->nchunk + 1) / 2);

@@ -319,7 +319,6 @@ ModParams device_mod(const bsattn_plan* p, const bsattn_score_mod* m, const DocW
 
 bsattn_status launch_doc_prep(const bsattn_plan* p, const bsattn_score_mod* m, const DocWs& w, cudaStream_t st) {
   if (!m->doc) return BSATTN_OK;
-  if (p->desc.B > 65535) return BSATTN_ERR_UNSUPPORTED;
   const long long chunks = (long long)p->N * p->nchunk;
   doc_prep_kernel<<<dim3((unsigned)((chunks + kPrepWarps - 1) / kPrepWarps), p->desc.B), 32 * kPrepWarps, 0, st>>>(
       make_geom(p), m->doc, w);
@@ -328,13 +327,18 @@ bsattn_status launch_doc_prep(const bsattn_plan* p, const bsattn_score_mod* m, c
 
 bsattn_status launch_mod_scores(const bsattn_plan* p, const ModParams& d, const float* S, float* out, cudaStream_t st) {
   const Geom g = make_geom(p);
-  if ((long long)g.B * g.Hh > 65535) return BSATTN_ERR_UNSUPPORTED;
   dim3 grid((g.N + 4 * kScoreThreads - 1) / (4 * kScoreThreads), (g.N + kScoreRows - 1) / kScoreRows, g.B * g.Hh);
   if (g.N % 4 == 0)  // every row starts on 16 bytes
     mod_scores_kernel<true><<<grid, kScoreThreads, 0, st>>>(g, d, S, out);
   else
     mod_scores_kernel<false><<<grid, kScoreThreads, 0, st>>>(g, d, S, out);
   return cudaGetLastError() == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+// What the rules on block scores refuse, asked before a call enqueues anything
+// (as check_attention_mod and check_backward_mod).
+bsattn_status check_scores(const bsattn_plan* p) {
+  return p->N > 2048 || (long long)p->desc.B * p->desc.heads > 65535 ? BSATTN_ERR_UNSUPPORTED : BSATTN_OK;
 }
 
 // The workspace of calls that need one for documents only.
@@ -368,6 +372,7 @@ bsattn_status forward_mod(const bsattn_plan* p, const bsattn_score_mod* m, const
     Carve c(ws);
     w = carve_forward_mod(p, c);
   }
+  if ((s = check_attention_mod(p))) return s;
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
   if ((s = launch_doc_prep(p, m, w.doc, (cudaStream_t)stream))) return s;
@@ -399,7 +404,7 @@ bsattn_status attn_mod_scores(const bsattn_plan* p, const bsattn_score_mod* m, c
   if (!p || !ok_ptr(S) || !ok_ptr(out)) return BSATTN_ERR_INVALID_ARG;
   bsattn_status s = check_mod(m);
   if (s) return s;
-  if (p->N > 2048) return BSATTN_ERR_UNSUPPORTED;
+  if ((s = check_scores(p))) return s;
   DocWs w;
   if ((s = carve_call_doc(p, m, ws, ws_bytes, &w))) return s;
   DeviceGuard dev(p->device);
@@ -435,6 +440,7 @@ bsattn_status attn_backward_mod(const bsattn_plan* p, const bsattn_score_mod* m,
   Carve size(nullptr);
   carve_backward_mod(p, size);
   if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+  if ((s = check_backward_mod(p))) return s;
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
   cudaStream_t st = (cudaStream_t)stream;
@@ -464,6 +470,9 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
   Carve size(nullptr);
   carve_layer_mod(p, size);
   if (!ws || !aligned16(ws) || ws_bytes < size.off) return BSATTN_ERR_WORKSPACE;
+  const bool route = p->rule.kind != BSATTN_RULE_WINDOW;
+  if ((s = m ? check_attention_mod(p) : check_attention(p))) return s;
+  if (m && route && (s = check_scores(p))) return s;
   DeviceGuard dev(p->device);
   if (dev.status) return dev.status;
   cudaStream_t st = (cudaStream_t)stream;
@@ -472,7 +481,6 @@ bsattn_status attn_layer_mod(const bsattn_plan* p, const bsattn_rope* rope, cons
   const Geom g = make_geom(p);
   int32_t* idx = idx_out ? idx_out : w.idx;
   int32_t* cnt = cnt_out ? cnt_out : w.cnt;
-  const bool route = p->rule.kind != BSATTN_RULE_WINDOW;
   const int32_t* doc = m ? m->doc : nullptr;
   const void *q = q_nat, *k = k_nat;
   if (m && (s = launch_doc_prep(p, m, w.doc, st))) return s;

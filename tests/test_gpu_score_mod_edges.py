@@ -131,3 +131,64 @@ def test_refused_frequencies_leave_everything_as_it_was(bs, rule):  # noqa: F811
         bs.attn_layer_mod(plan, r, bs.ScoreMod(softcap=5.0, doc=_docs(plan)), x, x, x, o, ws)
     assert e.value.code == 1
     assert torch.isnan(o).all() and torch.all(ws == 0xA5)
+
+
+BIG = {  # heads, D, grid, tile, window
+    "tiles": (1, 64, (32769, 1, 1), (1, 1, 1), (0, 0, 0)),      # more than 32768 tiles
+    "list": (1, 128, (1, 1033, 1), (1, 8, 1024), (0, 129, 0)),  # 16,640 steps of one block
+}
+
+
+@pytest.mark.parametrize("big", list(BIG))
+@pytest.mark.parametrize("call", ["forward", "forward_natural", "layer", "layer_no_rules"])
+def test_plans_too_large_for_the_forward(bs, big, call):  # noqa: F811
+    heads, D, grid, tile, win = BIG[big]
+    plan = bs.Plan(1, heads, D, *grid, rule="window", win=win, tile=tile)
+    x = torch.zeros(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")
+    o = _nan(plan.natural_shape())
+    mod = bs.ScoreMod(softcap=5.0, doc=_docs(plan))
+    layer = call.startswith("layer")
+    ws = _marked(plan.mod_info.layer_workspace_bytes if layer else plan.mod_info.forward_workspace_bytes)
+    si, sc = plan.list_shapes()
+    idx, cnt = torch.zeros(si, dtype=torch.int32, device="cuda"), torch.zeros(sc, dtype=torch.int32, device="cuda")
+    with pytest.raises(bs.BsattnError) as e:
+        if layer:
+            bs.attn_layer_mod(plan, bs.Rope(dims=(8, 8, 8)), mod if call == "layer" else None, x, x, x, o, ws)
+        elif call == "forward_natural":
+            bs.attn_forward_natural_mod(plan, mod, x, x, x, idx, cnt, o, ws)
+        else:
+            x = torch.empty(plan.tiled_shape(), dtype=torch.bfloat16, device="cuda")
+            o = _nan(plan.tiled_shape())
+            bs.attn_forward_mod(plan, mod, x, x, x, idx, cnt, o, ws)
+    assert e.value.code == 2
+    assert torch.isnan(o).all() and torch.all(ws == 0xA5)
+
+
+def test_plans_too_large_for_the_backward(bs):  # noqa: F811
+    """The dQ pass has room for its lists (128 steps), the dK, dV pass does not (8,192)."""
+    plan = bs.Plan(1, 1, 128, 1, 505, 1, rule="window", win=(0, 0, 0), tile=(1, 8, 1024))
+    x = torch.zeros(plan.tiled_shape(), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(plan.tiled_shape()[:-1], device="cuda")
+    idx = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 1, 64, 1)
+    cnt = torch.ones((1, 1, 64), dtype=torch.int32, device="cuda")
+    grads = [_nan(plan.tiled_shape()) for _ in range(3)]
+    ws = _marked(plan.mod_info.backward_workspace_bytes)
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_backward_mod(plan, bs.ScoreMod(softcap=5.0, doc=_docs(plan)), x, x, x, x, x, lse, idx, cnt, *grads, ws)
+    assert e.value.code == 2
+    assert all(torch.isnan(t).all() for t in grads) and torch.all(ws == 0xA5)
+
+
+def test_more_heads_than_the_rules_on_scores_take(bs):  # noqa: F811
+    plan = bs.Plan(300, 220, 64, 1, 1, 1, rule="topk", k=1)
+    s = torch.zeros((plan.B, plan.heads, 1, 1), device="cuda")
+    ws = _marked(plan.mod_info.scores_workspace_bytes)
+    mod = bs.ScoreMod(softcap=5.0, doc=_docs(plan))
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_mod_scores(plan, mod, s, s, ws)
+    assert e.value.code == 2 and torch.all(ws == 0xA5)
+    x = torch.zeros(plan.natural_shape(), dtype=torch.bfloat16, device="cuda")
+    o, ws = _nan(plan.natural_shape()), _marked(plan.mod_info.layer_workspace_bytes)
+    with pytest.raises(bs.BsattnError) as e:
+        bs.attn_layer_mod(plan, None, mod, x, x, x, o, ws)
+    assert e.value.code == 2 and torch.isnan(o).all() and torch.all(ws == 0xA5)
