@@ -242,6 +242,15 @@ class Plan:
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _device_tensor(name):
+    """A device tensor, or None, whose address stands in the field `name` of self.raw; may be exchanged."""
+    def exchange(self, t):
+        setattr(self.raw, name, _ptr(t))
+        setattr(self, "_" + name, t)
+
+    return property(lambda self: getattr(self, "_" + name), exchange)
+
+
 class Rope:
     """Rotary positions of Q and K (bsattn_rope in include/bsattn.h): `dims`
     features of each head turn with the token's t, h and w position. `pos`:
@@ -250,14 +259,15 @@ class Rope:
 
     LAYOUTS = {"interleaved": 0, "half": 1}
     SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+    pos = _device_tensor("pos")
 
     def __init__(self, dims, layout="interleaved", base=10000.0, scaling="none", factor=(1.0, 1.0, 1.0),
                  original=(1.0, 1.0, 1.0), slow=1.0, fast=32.0, amplitude=1.0, offset=(0, 0, 0), pos=None):
-        self.pos = pos
         self.raw = _Rope(self.LAYOUTS[layout] if isinstance(layout, str) else int(layout), tuple(int(d) for d in dims),
                          self.SCALINGS[scaling] if isinstance(scaling, str) else int(scaling), float(base),
                          tuple(float(f) for f in factor), tuple(float(x) for x in original), float(slow), float(fast),
-                         float(amplitude), tuple(int(o) for o in offset), _ptr(pos))
+                         float(amplitude), tuple(int(o) for o in offset), None)
+        self.pos = pos
 
     def _for(self, plan):
         if self.pos is not None:
@@ -270,12 +280,14 @@ class ScoreMod:
     tanh cap, distance bias (`slopes` fp32 [heads], `dist` weights of the
     distances along t, h, w), causal order of frames with a visible prefix
     (`prefix` int32 [B]) and document ids (`doc` int32 [B, L]). Holds on to
-    its tensors."""
+    its tensors; `slopes`, `prefix` and `doc` may be exchanged between calls."""
+
+    slopes, prefix, doc = (_device_tensor(name) for name in ("slopes", "prefix", "doc"))
 
     def __init__(self, softcap=0.0, slopes=None, dist=(1.0, 1.0, 1.0), causal=False, prefix=None, doc=None):
+        self.raw = _ScoreMod(float(softcap), float(dist[0]), float(dist[1]), float(dist[2]), None, int(bool(causal)),
+                             None, None)
         self.slopes, self.prefix, self.doc = slopes, prefix, doc
-        self.raw = _ScoreMod(float(softcap), float(dist[0]), float(dist[1]), float(dist[2]), _ptr(slopes),
-                             int(bool(causal)), _ptr(prefix), _ptr(doc))
 
     def _for(self, plan):
         for name, t, dtype, shape in (("slopes", self.slopes, torch.float32, (plan.heads,)),

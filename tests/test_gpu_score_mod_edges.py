@@ -1,5 +1,6 @@
 """Attention under score rules at its edges: references that move within a
-step, rows that are not numbers, and refusals, which come before any work."""
+step, rows that are not numbers, refusals, which come before any work, and
+tensors of a description exchanged between calls."""
 import math
 
 import numpy as np
@@ -192,3 +193,32 @@ def test_more_heads_than_the_rules_on_scores_take(bs):  # noqa: F811
     with pytest.raises(bs.BsattnError) as e:
         bs.attn_layer_mod(plan, None, mod, x, x, x, o, ws)
     assert e.value.code == 2 and torch.isnan(o).all() and torch.all(ws == 0xA5)
+
+
+# ---------------------------------------------------------------- tensors exchanged after construction
+
+def test_exchanged_tensors_are_used(bs):  # noqa: F811
+    c = Case(bs, "ragged", "all", seed=22)
+    plan, ws = c.plan, c.plan.workspace("mod_forward")
+
+    def run(mod):
+        o = _nan(plan.natural_shape())
+        bs.attn_forward_natural_mod(plan, mod, c.q.cuda(), c.k.cuda(), c.v.cuda(), c.idx, c.cnt, o, ws)
+        return o
+
+    old = [torch.zeros_like(t) for t in (c.mod.slopes, c.mod.prefix, c.mod.doc)]
+    mod = bs.ScoreMod(softcap=c.cap, slopes=old[0], dist=(1.0, 0.5, 0.0), causal=True, prefix=old[1], doc=old[2])
+    first = run(mod)
+    mod.slopes, mod.prefix, mod.doc = c.mod.slopes, c.mod.prefix, c.mod.doc
+    want = run(c.mod)
+    assert torch.equal(run(mod), want) and not torch.equal(first, want)
+    mod.slopes = mod.prefix = mod.doc = None
+    assert torch.equal(run(mod), run(bs.ScoreMod(softcap=c.cap, causal=True)))
+    with pytest.raises(ValueError):
+        mod.doc = c.mod.doc.cpu()
+    pos = torch.randint(-1000, 1000, (2, plan.B, plan.L, 3), device="cuda").to(torch.int32)
+    r, y = bs.Rope(dims=(8, 8, 8), pos=pos[0].clone()), [_nan(plan.natural_shape()) for _ in range(2)]
+    r.pos = pos[1]
+    bs.attn_rope(plan, r, c.q.cuda(), y[0])
+    bs.attn_rope(plan, bs.Rope(dims=(8, 8, 8), pos=pos[1]), c.q.cuda(), y[1])
+    assert torch.equal(y[0], y[1])
