@@ -4,7 +4,10 @@
 // Work unit, step list, rings and TMEM layout are those of the forward
 // without rules (csrc/attn_tc.cu): a 128-row query block of two 64-row chunks
 // walks the union of their kept key chunks, S = Q K^T (N = 64) and O += P V
-// per step, two CTAs per SM. Different is what stands between the products:
+// per step, two CTAs per SM (one where the plan's lists are longer than 1,300
+// steps at D = 128: list, coordinates and the table of chunk origins then take
+// more than half of the shared memory; 7,200 at D = 64, e4m3 3,500 and 6,200).
+// Different is what stands between the products:
 //
 //  * The step list is filtered by the rules at set-up (score_mod.cuh): chunks
 //    hidden from the whole block are never loaded, and only steps that need
@@ -492,14 +495,22 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool keep = ((e >> (30 + half)) & 1u) != 0;  // uniform within the warp
       unsigned long long vis = ~0ull;
       bool partial = false, clear = false;
-      const bool hidden_v = warp < 2 && (ext & mod::kHidden) != 0;  // this warp has V rows to look at
-      bool zero_v = false;                                          // row `tid` is a hidden token's
       mod::Dist dist{};
       if (BIAS || (ext & mod::kSpecial)) {
         const mod::Coord f = mod::chunk_first(g, M, ext, tab->at((int)((e >> 21) & 0x1FFu)));
         if (BIAS) dist = mod::make_dist(g, M, row.at, f, kFloor ? nslope / fmaxf(uks[n], least_ks) : nslope);
         if (ext & mod::kSpecial) {
-          if (hidden_v) zero_v = __ldg(M.doc_rows + 64 * step_chunk(e) + tid) < 0;
+          if ((ext & mod::kHidden) && warp < 2) {
+            // V rows of hidden tokens become zeros before the product reads them.
+            // Only once S_n is there: S_n follows PV_{n-2}, so the slot's barrier is
+            // past V_{n-2}, whose phase has the parity that stands for V_n's before.
+            const bool hidden = __ldg(M.doc_rows + 64 * step_chunk(e) + tid) < 0;
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait(bar_sfull(n & 1), (n >> 1) & 1, abort_flag, P.wait_limit) &&
+                                tc::mbar_wait(bar_vfull(n % kStages), (n / kStages) & 1, abort_flag, P.wait_limit));
+            if (ok && hidden) mod::zero_row(smem + C::OFF_V + (n % kStages) * C::V_BYTES, C::VBLK, tid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
           if (keep) {
             int vt = g.T - f.t;
             if (M.causal) vt = min(vt, max(row.at.t + 1, prefix) - f.t);
@@ -516,15 +527,6 @@ attn_mod_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       e = ulist[n1];
       ext = uext[n1];
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bar_sfull(n & 1), (n >> 1) & 1, abort_flag, P.wait_limit));
-      if (hidden_v) {
-        // V rows of hidden tokens become zeros before the product reads them.
-        // Only once S_n is there: S_n follows PV_{n-2}, so the slot's barrier is
-        // past V_{n-2}, whose phase has the parity that stands for V_n's before.
-        ok = ok && __all_sync(0xffffffffu,
-                              tc::mbar_wait(bar_vfull(n % kStages), (n / kStages) & 1, abort_flag, P.wait_limit));
-        if (ok && zero_v) mod::zero_row(smem + C::OFF_V + (n % kStages) * C::V_BYTES, C::VBLK, tid);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t sbuf = tmem + lane_base + ((n & 1) ? kColS1 : kColS0);
