@@ -20,16 +20,20 @@
 //              in fp32 and writes it as bf16 over the first 16 columns of its
 //              half of S.
 //   warp 8     TMA producer: Q and dO blocks once, then K_j and V_j together
-//              into a three-stage ring (a stage is released by the dQ MMA
-//              that last reads K_j).
-//   warp 9     MMA issuer (one thread): S_n = Q K_n^T and dP_n = dO V_n^T
-//              (both SS, N = 64) into double buffers, two steps ahead of the
-//              softmax side; dQ += dS_n K_n (dS from TMEM, K_n as an
-//              MN-major shared-memory operand).
-// TMEM (512 columns): S [0,64) and [64,128), dP [128,192) and [192,256),
-// dQ [256, 256+D). Every mbarrier wait is bounded; on expiry the CTA sets
-// the device error word, raises an abort flag, lets issued copies land,
-// drains its MMAs and frees TMEM.
+//              into a ring of three stages (a stage is released by the dQ MMA
+//              that last reads K_j); with score rules of four stages where the
+//              lists leave room (released by the S product two steps on).
+//   warp 9     MMA issuer (the warp runs as a whole, one elected lane issues,
+//              3.46 -> 2.69 ms with the rules; csrc/attn_mod_tc.cu has the
+//              reason): S_n = Q K_n^T and dP_n = dO V_n^T (both SS, N = 64)
+//              into double buffers, two steps ahead of the softmax side; dQ +=
+//              dS_n K_n (dS from TMEM, K_n as an MN-major shared-memory
+//              operand).
+// TMEM (512 columns): S [0,64) and [64,128), dP [128,192) and [192,256), dQ
+// [256, 256+D); with score rules dP [128,192), S's block operand [192,256), G
+// [384, 384+D). Every mbarrier wait is bounded; on expiry the CTA sets the
+// device error word, raises an abort flag, lets issued copies land, drains its
+// MMAs and frees TMEM.
 //
 // Under score rules dQ is computed first and corrects Delta on the way: the
 // rounding of O to bf16 puts an error eps_i into Delta_i, which costs dQ and
@@ -43,8 +47,7 @@
 // room for one dP buffer only; it is released as soon as the softmax side has
 // read it, and dS and P go over the two halves of S. On one B200 the backward
 // of the Wan-1.3B shape takes 2.48 ms without a rule, 3.01 with the cap, 3.54
-// with cap and bias (3.61 without rules on two dP buffers, one product fewer).
-// The MMA warp issues as a whole (csrc/attn_mod_tc.cu): 3.46 -> 2.69 ms.
+// with cap and bias (3.53 by attn_backward, two dP buffers, one product fewer).
 //
 // Score rules (MOD, score_mod.cuh): P is recomputed from the capped, biased
 // and masked scores; the step lists are filtered as in the forward. Hidden
@@ -807,7 +810,8 @@ bsattn_status run_dq(const bsattn_plan* p, const void* q, const void* k, const v
 //   dV += P^T dO_i and dK += dS^T Q_i (A from TMEM, dO_i and Q_i as MN-major
 //   shared-memory operands), accumulated in TMEM; dK is scaled at the end.
 // Per step the TMA warp brings Q_i, dO_i and the 64 lse and Delta values of
-// query tile i into a three-stage ring.
+// query tile i into a ring of three stages, with score rules of four where the
+// lists leave room.
 struct KvParams {
   Geom g;
   const int32_t* idxT;  // [B, Hh, N, N] query tiles keeping each key tile, ascending

@@ -20,9 +20,11 @@
 //
 // Measured on one B200 (measured copy rate 6,528 GB/s): Q and K of the
 // Wan-1.3B-shaped layer with means 59 us (291 MB, 0.75 of the copy rate; 3.7
-// waves of CTAs), the Wan-14B-shaped gradient in the half layout 576-594 us
-// (3.10 GB, 0.80-0.82), one token 3.8 us. A thread per column of all heads,
-// with angles from fp64, took 84 us, 669 us and 4-36 us; two heads a thread
+// waves of CTAs), the Wan-14B-shaped gradient in the half layout 560-597 us
+// (3.10 GB, 0.79-0.85), one token 3.8 us; at that size explicit positions take
+// 670-740 us (a table row per token row) and half layouts with R no multiple
+// of 8 980 us (features two by two). A thread per column of all heads, with
+// angles from fp64, took 84 us, 669 us and 4-36 us; two heads a thread
 // instead of four 743 us in the half layout (twice the table reads per
 // feature, half the contiguous bytes).
 #include "internal.h"
@@ -63,8 +65,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 //   kHalf8:       features [8u, 8u + 8) and [R + 8u, R + 8u + 8) (8
 //                 pairs), R a multiple of 8; 8 passed features each   (D - R) / 8 units
 //   kPair:        two features: a pair, or two passed ones; for half
-//                 layouts whose R is not a multiple of 8 (2-byte
-//                 accesses: 4x the load instructions of kHalf8)       D / 2 units
+//                 layouts whose R is not a multiple of 8, where a
+//                 pair's features share no 16-byte alignment (2-byte
+//                 accesses: 980 us where kHalf8 with R = 40 takes 560) D / 2 units
 enum Mode { kInterleaved, kHalf8, kPair };
 constexpr int kHeads = 4;  // heads of a CTA
 constexpr uint32_t kHiddenRow = 1u << 31;
@@ -364,7 +367,8 @@ bsattn_status check_rope(const bsattn_plan* p, const bsattn_rope* r, RopeTurns* 
     const double s = r->factor[a];
     double base = r->base;
     if (r->scaling == BSATTN_ROPE_SCALE_NTK && d > 2) base *= pow(s, (double)d / (d - 2));
-    // exp2 of the rounded exponent: within 1e-7 of a radian at position 2^31.
+    // Frequencies of 53 bits: up to 1 they are within 4e-7 of a radian at position
+    // 2^31 (3.1e-7 is the most that bases of 100 to 10^6 give unscaled).
     const double per_pair = d > 0 ? -2.0 * log2(base) / d : 0.0;
     for (int i = 0; i < d / 2; ++i) {
       double f = exp2(per_pair * i);

@@ -142,10 +142,11 @@ __device__ __forceinline__ void list_steps(const Geom& g, const uint32_t* bmA, c
   if (tid == 0) *count = (uint32_t)min(tot, cap);
 }
 
-// Turns the first part of an ascending list, the steps up to the query tile,
-// around: a walk then starts at the query tile and leaves it in both
+// Turns the first part of an ascending list, the steps up to the block's first
+// query tile, around: a walk then starts there and leaves it in both
 // directions, so that under a distance bias the nearest keys come first and a
-// row's reference, set by its first keys, seldom has to move.
+// row's reference, set by its first keys, seldom has to move. (Rows of the
+// block's second tile start at their neighbour.)
 template <int NT>
 __device__ __forceinline__ void nearest_first(uint32_t* list, uint32_t* ext, int steps, int tile) {
   int lo = 0, hi = steps;  // steps of tiles <= tile

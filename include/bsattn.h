@@ -353,9 +353,11 @@ bsattn_status attn_schedule_layer(const bsattn_schedule* schedule, int step, con
  *             0, 1), r_i = original * f_i / (2 pi): pairs that turn more than
  *             `fast` times over the original extent keep their frequency,
  *             those that turn fewer than `slow` times are interpolated.
- * Angles are formed in fp64 (exact for every int32 position up to its last
- * bits) and reduced before sine and cosine are taken in fp32; the rotation is
- * fp32, rounded to bf16 once. */
+ * Frequencies are formed in fp64 and held as 64-bit binary fractions of a
+ * turn, so that a position times a frequency wraps by whole turns in integer
+ * arithmetic: with frequencies up to 1, angles are within 4e-7 of a radian for
+ * every int32 position (in proportion to higher frequencies). Sine, cosine and
+ * the rotation are fp32, rounded to bf16 once. */
 typedef enum { BSATTN_ROPE_INTERLEAVED = 0, BSATTN_ROPE_HALF = 1 } bsattn_rope_layout;
 typedef enum {
   BSATTN_ROPE_SCALE_NONE = 0,
@@ -403,9 +405,10 @@ bsattn_status attn_rope(const bsattn_plan* plan, const bsattn_rope* rope, const 
  * token with a negative id is hidden altogether: what its Q, K, V and dO
  * rows hold, NaN and infinities included, does not reach any other row (tile
  * scales of the e4m3 path must be positive and finite, as attn_quantize_e4m3
- * makes them of finite values; attn_layer_mod makes them without such tokens). Values at pairs that only `causal` or two different ids hide
- * must be finite. A sequence is a grid of one column (T = length, H = W = 1,
- * tiles of (64, 1, 1)). */
+ * makes them of finite values; attn_layer_mod makes them without such tokens).
+ * Values at pairs that only `causal` or two different ids hide must be finite.
+ * A visible query row that holds a NaN has O and lse NaN. A sequence is a grid
+ * of one column (T = length, H = W = 1, tiles of (64, 1, 1)). */
 typedef struct {
   float softcap;                 /* 0: off; else in [1e-6, 1e30]              */
   float dist_t, dist_h, dist_w;  /* >= 0, finite                              */
@@ -431,17 +434,21 @@ bsattn_status attn_mod_info(const bsattn_plan* plan, bsattn_mod_info* out);
  * a whole are those with no frame of the key tile visible to a frame of the
  * query tile, and those whose ranges [least, greatest] of ids >= 0 do not
  * meet (exact for ids that do not decrease along the tokens, never too much).
- * `out` may be `scores`. UNSUPPORTED: N above 2048. `ws`:
- * scores_workspace_bytes; may be NULL without doc. */
+ * `out` may be `scores`. UNSUPPORTED: N above 2048, B * heads above 65535.
+ * `ws`: scores_workspace_bytes; may be NULL without doc. */
 bsattn_status attn_mod_scores(const bsattn_plan* plan, const bsattn_score_mod* mod, const float* scores,
                               float* out, void* ws, size_t ws_bytes, void* stream);
 
-/* attn_forward and attn_forward_natural under score rules (any plan; cap,
- * bias and masks are applied in fp32 inside the kernel, and key chunks that
- * the rules hide from a whole query block are not visited). Padded rows of
- * the tiled layout get O = 0, lse = -inf. `ws`: forward_workspace_bytes; may
- * be NULL without doc, and then small problems, whose query blocks several
- * CTAs share through it, take longer and round differently. */
+/* attn_forward and attn_forward_natural under score rules (cap, bias and
+ * masks are applied in fp32 inside the kernel, and key chunks that the rules
+ * hide from a whole query block are not visited). Padded rows of the tiled
+ * layout get O = 0, lse = -inf. `ws`: forward_workspace_bytes; may be NULL
+ * without doc, and then small problems, whose query blocks several CTAs share
+ * through it, take longer and round differently. UNSUPPORTED: N above 32768,
+ * B or heads above 65535, 2^31 - 128 tiled rows or more, and lists too long
+ * for a block's shared memory: the 64-key chunks that two neighbouring query
+ * tiles (one tile of several chunks) can keep, above about 15,400 for head_dim
+ * 128 and 21,400 for 64 (e4m3: 13,000 and 15,700). */
 bsattn_status attn_forward_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
                                const void* k, const float* q_scale, const float* k_scale, const void* v,
                                const int32_t* idx, const int32_t* cnt, void* o_tiled, float* lse, void* ws,
@@ -453,10 +460,15 @@ bsattn_status attn_forward_natural_mod(const bsattn_plan* plan, const bsattn_sco
 
 /* Backward of attn_forward_mod (same rules, o and lse from it), as
  * attn_backward: dZ = P * (dO V^T - rowsum(dO * O)), the capped scores'
- * derivative 1 - tanh^2 on top for dQ and dK; d_slopes, if non-NULL (fp32
- * [heads], needs mod->slopes), gets -sum dZ * distance over the batch, summed
- * in a fixed order. Gradients of hidden tokens and padded rows are zero.
- * UNSUPPORTED for qk_fp8 plans. `ws`: backward_workspace_bytes. */
+ * derivative 1 - tanh^2 on top for dQ and dK (formed in fp32 from the tanh,
+ * within about 1e-6 of its exact value, so it has few digits left where a
+ * score is above six caps); d_slopes, if non-NULL (fp32 [heads], needs
+ * mod->slopes), gets -sum dZ * distance over the batch, summed in a fixed
+ * order. Gradients of hidden tokens and padded rows are zero. UNSUPPORTED:
+ * qk_fp8 plans, B or heads above 65535, 2^31 - 128 tiled rows or more, and
+ * grids or lists too long for a block's shared memory: 64-row chunks in all
+ * tiles, above about 7,100 for head_dim 128 and 17,000 for 64. `ws`:
+ * backward_workspace_bytes. */
 bsattn_status attn_backward_mod(const bsattn_plan* plan, const bsattn_score_mod* mod, const void* q,
                                 const void* k, const void* v, const void* o, const void* d_o,
                                 const float* lse, const int32_t* idx, const int32_t* cnt, void* dq, void* dk,
@@ -469,7 +481,7 @@ bsattn_status attn_backward_mod(const bsattn_plan* plan, const bsattn_score_mod*
  * attn_mod_scores, attn_select_from_scores, attn_quantize_e4m3 on an e4m3
  * plan, attn_forward_natural_mod), except that tokens with a negative id enter
  * no tile mean (a tile of such tokens has mean 0) and no e4m3 tile scale.
- * `ws`: attn_mod_info's layer_workspace_bytes. */
+ * UNSUPPORTED as those calls. `ws`: attn_mod_info's layer_workspace_bytes. */
 bsattn_status attn_layer_mod(const bsattn_plan* plan, const bsattn_rope* rope, const bsattn_score_mod* mod,
                              const void* q_nat, const void* k_nat, const void* v_nat, void* o_nat,
                              float* lse_nat, int32_t* idx_out, int32_t* cnt_out, void* ws, size_t ws_bytes,
